@@ -412,6 +412,57 @@ int attn_decode_q8(const void *q, int32_t q_dtype, const void *k8_cache, const v
 size_t attn_decode_q8_workspace_bytes(int32_t batch, const int64_t *ctx_len, int32_t window);
 int attn_dot_canary(void *stream, int32_t *variant);
 
+/*
+ * attn_norm_rope_append -- the whole step between the q / k / v projections
+ * and the attention calls: RMS norm of every query head, of the key and of
+ * the value, rotation of queries and key by position, the queries written out
+ * and K / V written into the cache, in one pass.  For a row x of 256 values:
+ *   norm      y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)
+ *             (w = 1 and no offset where the weight is NULL, and for V)
+ *   rotation  a_i = pos[axis_i] * inv_freq[i]                       (i < 128)
+ *             z[i]       = y[i] cos a_i - y[i+128] sin a_i
+ *             z[i + 128] = y[i+128] cos a_i + y[i] sin a_i
+ * Statistics and products are f32, angles f64 (far positions keep the
+ * fraction of a turn), and each value is rounded once, to nearest even, to
+ * the type it is stored in.  The release notes have no counterpart to this
+ * fused call (attn_append_kv is the pages' append, with host cos/sin rows).
+ *   q            n_rows tokens of [8][256] in_dtype, q_stride elements apart
+ *   k_new/v_new  n_rows tokens of [256] in_dtype, k_stride / v_stride elements
+ *                apart.  Strides are 0..2^32 and whole 16-byte units, so q, k
+ *                and v may be slices of one projection's output, or one row
+ *                for all tokens (stride 0)
+ *   flags        KCA_NORM_QK: norm q and k; KCA_NORM_V: norm v; 0: neither
+ *   q_weight/k_weight  [256] w_dtype, device, 16-byte aligned, or NULL
+ *   eps          finite, >= 0
+ *   positions    DEVICE int64 [n_axes][n_rows], any values; NULL together with
+ *                inv_freq: no rotation
+ *   n_axes       1..KCA_MAX_ROPE_AXES (time, height, width, ...)
+ *   freq_axis    HOST uint8 [128], the axis each frequency follows, or NULL
+ *                (all follow axis 0)
+ *   inv_freq     DEVICE f32 [128], radians per position, 16-byte aligned; 0
+ *                leaves the pair as it is (partial rotation)
+ *   q_out        [n_rows][8][256] q_out_dtype; may be q itself when q is
+ *                contiguous and of q_out_dtype (KCA_ERR_RANGE otherwise)
+ *   k_cache/v_cache, kv_dtype, cache_rows, dst_rows_dev, dst_row0, workspace
+ *                as in attn_append_kv, except that a device destination of -1
+ *                marks a padding token: nothing of it is read or written
+ *                (q_out included), and that is no error.  Any other
+ *                destination outside the cache skips the token likewise and is
+ *                recorded (error bit 3, value 4).
+ * Returns KCA_OK or a KCA_ERR_* before launching anything.
+ */
+#define KCA_NORM_QK 1
+#define KCA_NORM_V 2
+#define KCA_MAX_ROPE_AXES 4
+int attn_norm_rope_append(const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
+                          const void *v_new, int64_t v_stride, int32_t in_dtype, int32_t n_rows,
+                          int32_t flags, const void *q_weight, const void *k_weight, int32_t w_dtype,
+                          float weight_offset, float eps, const int64_t *positions, int32_t n_axes,
+                          const uint8_t *freq_axis, const float *inv_freq, void *q_out,
+                          int32_t q_out_dtype, void *k_cache, void *v_cache, int32_t kv_dtype,
+                          int64_t cache_rows, const int64_t *dst_rows_dev, int64_t dst_row0,
+                          void *workspace, void *stream);
+
 /* Workspace bytes the calls above need on the current device (0 on a bad
  * argument).  Always >= KCA_WORKSPACE_HEADER.  The size depends on the
  * device (its SM count sets the split plan), so it is asked of the device the

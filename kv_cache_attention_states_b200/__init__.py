@@ -10,6 +10,7 @@ library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,6 +26,7 @@ I8_ROW_BYTES = 272        # packed int8 K row: 256 codes, f32 scale, 12 zero byt
 N_Q_HEADS, N_KV_HEADS, HEAD_DIM = 8, 1, 256
 MAX_CHUNK_ROWS, MAX_POSITION, MAX_BATCH, MAX_BATCH_ROWS = 768, 131072, 256, 15
 WORKSPACE_HEADER = 24832  # status word + per-(row, head) merge counters
+NORM_QK, NORM_V, MAX_ROPE_AXES = 1, 2, 4
 STATUS = {0: "KCA_OK", -1: "KCA_ERR_NULL", -2: "KCA_ERR_GEOMETRY", -3: "KCA_ERR_DTYPE",
           -4: "KCA_ERR_RANGE", -5: "KCA_ERR_WORKSPACE", -6: "KCA_ERR_ALIGN", -7: "KCA_ERR_CUDA",
           -8: "KCA_ERR_DEVICE"}
@@ -110,6 +112,9 @@ def load_library(path: str) -> ctypes.CDLL:
     L.attn_dot_canary.restype = ctypes.c_int
     L.attn_decode_cluster_capacity.argtypes = [p32]
     L.attn_decode_cluster_capacity.restype = ctypes.c_int
+    L.attn_norm_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, f32, f32, vp, i32, vp,
+                                        vp, vp, i32, vp, vp, i32, i64, vp, i64, vp, vp]
+    L.attn_norm_rope_append.restype = ctypes.c_int
     L.attn_force_path.argtypes = [i32, i32]
     L.attn_force_path.restype = ctypes.c_int
     L.attn_status_string.argtypes = [ctypes.c_int]
@@ -168,6 +173,26 @@ def _i64_array(vals):
 def _check(status: int, what: str):
     if status != 0:
         raise KcaError(status, what)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The library works on the current device: makes `device` it for a call."""
+    import torch
+    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+def _need(device, **tensors):
+    """Each tensor (None is skipped) contiguous and on the CUDA device `device`."""
+    for name, t in tensors.items():
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor on {device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ----------------------------------------------------------------- workspace
@@ -449,6 +474,90 @@ def attn_append_kv(k_new, v_new, k_cache, v_cache, dst, rope_cos=None, rope_sin=
                               vp(workspace.data_ptr()) if workspace is not None else None,
                               _stream_ptr(stream))
     _check(st, "attn_append_kv")
+
+
+_FREQ_AXIS = {}
+
+
+def _freq_axis(freq_axis, n_axes: int):
+    """The axis of each of the 128 frequencies as a C byte array (made once
+    per distinct assignment), or None."""
+    if freq_axis is None:
+        return None
+    key = bytes(freq_axis)
+    if len(key) != HEAD_DIM // 2 or max(key) >= n_axes:
+        raise ValueError(f"freq_axis must give one of {n_axes} axes for each of 128 frequencies")
+    arr = _FREQ_AXIS.get(key)
+    if arr is None:
+        if len(_FREQ_AXIS) >= 64:
+            _FREQ_AXIS.clear()
+        arr = _FREQ_AXIS[key] = (ctypes.c_uint8 * len(key)).from_buffer_copy(key)
+    return arr
+
+
+def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None, inv_freq=None, freq_axis=None,
+                          q_weight=None, k_weight=None, weight_offset: float = 0.0, eps: float = 1e-6,
+                          norm_qk: bool = True, norm_v: bool = False, q_out=None, workspace=None, stream=None):
+    """Norm of every query head, key (and value), rotation by position, K/V
+    append, in one pass; returns the queries.
+
+    q: [n, 8, 256] and k_new / v_new: [n, 256] (or [n, 1, 256]), one dtype, each
+    token's values contiguous and tokens any (16-byte) stride apart, so slices
+    of one projection's output serve; k_cache / v_cache, dst and workspace as in
+    attn_append_kv, a device destination of -1 marking a padding token that is
+    skipped; positions: int64 CUDA [n] or [axes, n] (axes <= 4) with inv_freq
+    float32 CUDA [128] (radians per position, 0: not rotated) and freq_axis 128
+    axis numbers (None: axis 0), or None for no rotation; q_weight / k_weight:
+    [256] of one dtype; q_out: contiguous [n, 8, 256] of any dtype (default: new,
+    of the cache's), or q itself.
+    """
+    import torch
+    n, dev = q.shape[0], q.device
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    if q.shape[1:] != (N_Q_HEADS, HEAD_DIM) or q.stride(2) != 1 or q.stride(1) != HEAD_DIM:
+        raise ValueError("q must be [n, 8, 256] with each token's values contiguous")
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if (t.device != dev or t.dtype != q.dtype or t.shape[0] != n or t.shape[-1] != HEAD_DIM
+                or (t.dim() != 2 and (t.dim() != 3 or t.shape[1] != 1)) or t.stride(-1) != 1):
+            raise ValueError(f"{name} must be [n, 256] of q's dtype on {dev}, each token's values contiguous")
+    _need(dev, k_cache=k_cache, v_cache=v_cache, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+          k_weight=k_weight, q_out=q_out, workspace=workspace)
+    if k_cache.dtype != v_cache.dtype or k_cache.shape[-1] != HEAD_DIM or v_cache.numel() != k_cache.numel():
+        raise ValueError("k_cache and v_cache must be alike, with a last axis of 256")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("give both positions and inv_freq, or neither")
+    n_axes = 1
+    if positions is not None:
+        n_axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.dtype != torch.int64 or positions.dim() > 2 or positions.numel() != n_axes * n or positions.shape[-1] != n:
+            raise ValueError("positions must be int64 [n] or [axes, n]")
+        if inv_freq.dtype != torch.float32 or inv_freq.numel() != HEAD_DIM // 2:
+            raise ValueError("inv_freq must be float32 [128]")
+    wt = q_weight if q_weight is not None else k_weight
+    for t in (q_weight, k_weight):
+        if t is not None and (t.numel() != HEAD_DIM or t.dtype != wt.dtype):
+            raise ValueError("q_weight and k_weight must be [256] of one dtype")
+    if q_out is None:
+        q_out = torch.empty((n, N_Q_HEADS, HEAD_DIM), dtype=k_cache.dtype, device=dev)
+    if q_out.numel() != n * N_Q_HEADS * HEAD_DIM:
+        raise ValueError("q_out must be [n, 8, 256]")
+    if isinstance(dst, int):
+        dst_p, dst0 = None, dst
+    else:
+        if dst.dtype != torch.int64 or dst.device != dev or dst.numel() != n or not dst.is_contiguous():
+            raise ValueError("dst must be an int or a contiguous int64 CUDA tensor [n]")
+        dst_p, dst0 = dst.data_ptr(), 0
+    with _on(dev):
+        st = lib().attn_norm_rope_append(
+            q.data_ptr(), q.stride(0), k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
+            dtype_code(q), n, (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), _ptr(q_weight), _ptr(k_weight),
+            F32 if wt is None else dtype_code(wt), weight_offset, eps, _ptr(positions), n_axes,
+            _freq_axis(freq_axis, n_axes), _ptr(inv_freq), q_out.data_ptr(), dtype_code(q_out), k_cache.data_ptr(),
+            v_cache.data_ptr(), dtype_code(k_cache), k_cache.numel() // HEAD_DIM, dst_p, dst0, _ptr(workspace),
+            _stream_ptr(stream, dev))
+    _check(st, "attn_norm_rope_append")
+    return q_out
 
 
 # ------------------------------------------------------- quantised-dot decode

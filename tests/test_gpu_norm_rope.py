@@ -1,0 +1,284 @@
+"""GPU parity of attn_norm_rope_append (norm of q, k and v, rotation by position,
+append) against the f64 oracle: types, strided slices of one projection,
+several position axes, far positions, padding tokens, a captured step, another
+stream, and the run into attn_decode_dev that a decode step makes of it."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_attention_states_b200 as kca
+from kv_cache_attention_states_b200 import synth
+from oracle import norm_rope
+from oracle.partial import decode_partial, widen
+from tests.helpers import dev, max_err, tol
+
+pytestmark = pytest.mark.gpu
+
+# half a step of each type, relative to the value, and its smallest half step
+HALF_STEP = {"f32": (2.0 ** -24, 2.0 ** -150), "f16": (2.0 ** -11, 2.0 ** -25), "bf16": (2.0 ** -8, 2.0 ** -134)}
+# The f32 computation, relative to the length of a rotated pair: the sum of
+# squares (8 fused steps and 5 additions of positive terms: 13 roundings, half
+# of them after the root), the mean, eps, root and quotient (4), two products
+# for the weight and its offset (3), the angle (a remainder of at most half a
+# turn rounded to f32 and doubled: 2 pi 2^-26 a rounding, 1.6; sincospif 2 ulp
+# of at most 2^-24 each: 4), and the products and sum of the rotation (3, by
+# sqrt 2): below 26 roundings of 2^-24.
+COMPUTE = 26 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup(cuda_ok):
+    kca.lib()
+
+
+def _close(got, dtype, want, length):
+    rel, least = HALF_STEP[dtype]
+    err = np.abs(widen(got, dtype) - want)
+    bound = rel * (np.abs(want) + COMPUTE * length) + COMPUTE * length + least
+    worst = float(np.max(err / bound))
+    assert worst <= 1.0, worst
+
+
+def _host(t):
+    t = t.cpu().contiguous()
+    return t.view(torch.int16).numpy().view(np.uint16) if t.dtype == torch.bfloat16 else t.numpy()
+
+
+def _freq(axes, theta=1e4):
+    inv = (theta ** (-np.arange(128) / 128.0)).astype(np.float32)
+    inv[-7:] = 0.0
+    return inv, [i % axes for i in range(128)]
+
+
+class Case:
+    """Random inputs of n tokens and the oracle's answer."""
+
+    def __init__(self, seed, n, dt, axes=1, far=5000, weights=True, w_dt="f32", std=1.5, **kw):
+        self.n, self.dt = n, dt
+        self.q = synth.draw(seed, "q", (n, 8, 256), dt, std)
+        self.k = synth.draw(seed, "k", (n, 256), dt, std)
+        self.v = synth.draw(seed, "v", (n, 256), dt, std)
+        self.pos = synth.integers(seed, "pos", 0, far, axes * n).reshape(axes, n)
+        self.inv, self.axis = _freq(axes)
+        self.wq = synth.draw(seed, "wq", (256,), w_dt, 0.3) if weights else None
+        self.wk = synth.draw(seed, "wk", (256,), w_dt, 0.3) if weights else None
+        self.w_dt, self.kw = w_dt, kw
+
+    def want(self, rotate=True):
+        kw = dict(self.kw)
+        return norm_rope.norm_rope(
+            self.q, self.k, self.v, self.dt, pos=self.pos if rotate else None, inv_freq=self.inv, axis=self.axis,
+            wq=None if self.wq is None else widen(self.wq, self.w_dt),
+            wk=None if self.wk is None else widen(self.wk, self.w_dt), w0=kw.pop("weight_offset", 0.0), **kw)
+
+    def args(self, rotate=True):
+        d = dict(self.kw)
+        if rotate:
+            d.update(positions=torch.from_numpy(self.pos).cuda(), inv_freq=torch.from_numpy(self.inv).cuda(),
+                     freq_axis=self.axis)
+        if self.wq is not None:
+            d.update(q_weight=dev(self.wq, self.w_dt), k_weight=dev(self.wk, self.w_dt))
+        return d
+
+
+def _caches(seed, rows, kv):
+    return (synth.draw(seed, "kc", (rows, 256), kv), synth.draw(seed, "vc", (rows, 256), kv))
+
+
+def _check(case, got_q, q_dt, kd, vd, kv, old_k, old_v, dst, rotate=True, skip=()):
+    want, length = case.want(rotate)
+    keep = np.array([t not in skip for t in range(case.n)])
+    _close(_host(got_q)[keep], q_dt, want[keep, :8], length[keep, :8])
+    k, v = _host(kd), _host(vd)
+    _close(k[dst[keep]], kv, want[keep, 8], length[keep, 8])
+    _close(v[dst[keep]], kv, want[keep, 9], length[keep, 9])
+    other = np.ones(k.shape[0], dtype=bool)
+    other[dst[keep]] = False
+    assert np.array_equal(k[other], old_k[other]) and np.array_equal(v[other], old_v[other])
+
+
+@pytest.mark.parametrize("dt,kv,q_dt", [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("f32", "f32", "f32"),
+                                        ("f32", "f16", "f16"), ("bf16", "f32", "f16")])
+@pytest.mark.parametrize("n", [1, 3, 512, 513, 1030])
+@pytest.mark.parametrize("norm_v", [False, True])
+def test_types_and_lengths(dt, kv, q_dt, n, norm_v):
+    case = Case(11, n, dt, axes=1, w_dt="f32" if dt == "f32" else dt, norm_v=norm_v)
+    rows = n + 9
+    old_k, old_v = _caches(12, rows, kv)
+    kd, vd = dev(old_k, kv), dev(old_v, kv)
+    q_out = torch.empty((n, 8, 256), dtype=synth.torch_dtype(q_dt), device="cuda")
+    got = kca.attn_norm_rope_append(dev(case.q, dt), dev(case.k, dt), dev(case.v, dt), kd, vd, 4, q_out=q_out,
+                                    **case.args())
+    assert got is q_out
+    _check(case, got, q_dt, kd, vd, kv, old_k, old_v, np.arange(4, 4 + n))
+
+
+@pytest.mark.parametrize("axes,far", [(1, 131071), (2, 3000), (3, 40000), (4, 131071)])
+@pytest.mark.parametrize("n", [5, 700])
+def test_position_axes_and_scattered_destinations(axes, far, n):
+    case = Case(13, n, "bf16", axes=axes, far=far, w_dt="bf16", weight_offset=1.0, eps=1e-5)
+    rows = 2 * n + 1
+    old_k, old_v = _caches(14, rows, "bf16")
+    kd, vd = dev(old_k, "bf16"), dev(old_v, "bf16")
+    dst = np.random.default_rng(5).permutation(rows)[:n]
+    got = kca.attn_norm_rope_append(dev(case.q, "bf16"), dev(case.k, "bf16"), dev(case.v, "bf16"), kd, vd,
+                                    torch.from_numpy(dst).cuda(), **case.args())
+    _check(case, got, "bf16", kd, vd, "bf16", old_k, old_v, dst)
+
+
+@pytest.mark.parametrize("rotate,norm_qk,weights", [(False, True, True), (True, False, False), (False, False, False),
+                                                    (True, True, False)])
+@pytest.mark.parametrize("n", [2, 600])
+def test_parts_left_out(rotate, norm_qk, weights, n):
+    case = Case(15, n, "f32", weights=weights, norm_qk=norm_qk)
+    old_k, old_v = _caches(16, n, "f16")
+    kd, vd = dev(old_k, "f16"), dev(old_v, "f16")
+    got = kca.attn_norm_rope_append(dev(case.q, "f32"), dev(case.k, "f32"), dev(case.v, "f32"), kd, vd, 0,
+                                    **case.args(rotate))
+    _check(case, got, "f16", kd, vd, "f16", old_k, old_v, np.arange(n), rotate)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 77, 777])
+def test_slices_of_one_projection(dt, n):
+    """q, k and v as strided slices of a [n, 2576] buffer (16 columns spare)."""
+    case = Case(17, n, dt)
+    buf = torch.full((n, 10 * 256 + 16), 7.0, dtype=synth.torch_dtype(dt), device="cuda")
+    buf[:, :2048] = dev(case.q, dt).reshape(n, 2048)
+    buf[:, 2048:2304] = dev(case.k, dt)
+    buf[:, 2304:2560] = dev(case.v, dt)
+    old_k, old_v = _caches(18, n, "bf16")
+    kd, vd = dev(old_k, "bf16"), dev(old_v, "bf16")
+    got = kca.attn_norm_rope_append(buf[:, :2048].unflatten(1, (8, 256)), buf[:, 2048:2304], buf[:, 2304:2560], kd, vd,
+                                    0, **case.args())
+    _check(case, got, "bf16", kd, vd, "bf16", old_k, old_v, np.arange(n))
+
+
+def test_one_key_row_for_all_tokens_and_queries_in_place():
+    n = 6
+    case = Case(19, n, "f16")
+    case.k[:] = case.k[:1]
+    case.v[:] = case.v[:1]
+    old_k, old_v = _caches(20, n, "f16")
+    kd, vd = dev(old_k, "f16"), dev(old_v, "f16")
+    q = dev(case.q, "f16")
+    got = kca.attn_norm_rope_append(q, dev(case.k[:1], "f16").expand(n, 256), dev(case.v[:1], "f16").expand(n, 256), kd,
+                                    vd, 0, q_out=q, **case.args())
+    assert got.data_ptr() == q.data_ptr()
+    _check(case, got, "f16", kd, vd, "f16", old_k, old_v, np.arange(n))
+
+
+def test_queries_in_place_need_their_own_layout():
+    q = torch.zeros((4, 8, 256), dtype=torch.float16, device="cuda")
+    kv = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
+    cache = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
+    with pytest.raises(kca.KcaError):   # one query row for all tokens cannot be written by each
+        kca.attn_norm_rope_append(q[:1].expand(4, 8, 256), kv, kv, cache, cache.clone(), 0, q_out=q)
+    with pytest.raises(kca.KcaError):   # another type over the same bytes
+        kca.attn_norm_rope_append(q, kv, kv, cache, cache.clone(), 0, q_out=q.view(torch.bfloat16))
+
+
+@pytest.mark.parametrize("n", [9, 600])
+def test_padding_tokens_and_bad_destinations(n):
+    case = Case(21, n, "bf16")
+    rows = n + 3
+    old_k, old_v = _caches(22, rows, "bf16")
+    kd, vd = dev(old_k, "bf16"), dev(old_v, "bf16")
+    dst = np.arange(n, dtype=np.int64)
+    dst[[0, n - 1]] = -1
+    ws = kca.new_workspace(kca.WORKSPACE_HEADER)
+    q_out = torch.full((n, 8, 256), 3.0, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        return kca.attn_norm_rope_append(dev(case.q, "bf16"), dev(case.k, "bf16"), dev(case.v, "bf16"), kd, vd,
+                                         torch.from_numpy(dst).cuda(), q_out=q_out, workspace=ws, **case.args())
+
+    got = call()
+    _check(case, got, "bf16", kd, vd, "bf16", old_k, old_v, dst, skip=(0, n - 1))
+    assert bool((got[[0, n - 1]] == 3.0).all())
+    assert kca.attn_device_status(ws)[0] == 0           # padding is no error
+    dst[3], dst[5] = rows, -2
+    before = _host(kd).copy(), _host(vd).copy()         # rows 3 and 5 keep what the first call wrote
+    got = call()
+    _check(case, got, "bf16", kd, vd, "bf16", *before, dst, skip=(0, 3, 5, n - 1))
+    st, detail = kca.attn_device_status(ws)
+    assert st == -8 and detail >> 24 == 11 and detail & 0xFFFFFF in (3, 5)
+
+
+def test_zero_and_large_rows():
+    """A zero row stays zero (eps > 0); values near the top of f16 do not
+    overflow the f32 statistics."""
+    case = Case(23, 4, "f16", std=1.0, weights=False)
+    case.q[0], case.k[1], case.q[2, 3] = 0, 0, 65504
+    old_k, old_v = _caches(24, 4, "f32")
+    kd, vd = dev(old_k, "f32"), dev(old_v, "f32")
+    got = kca.attn_norm_rope_append(dev(case.q, "f16"), dev(case.k, "f16"), dev(case.v, "f16"), kd, vd, 0, **case.args())
+    assert bool((got[0] == 0).all()) and bool((kd[1] == 0).all())
+    _check(case, got, "f32", kd, vd, "f32", old_k, old_v, np.arange(4))
+
+
+def test_far_and_negative_positions_keep_the_fraction_of_a_turn():
+    case = Case(25, 8, "f32", weights=False)
+    case.pos[0] = [2 ** 31 + 5, -7, 10 ** 9, -(2 ** 40) - 3, 0, 1, -1, 2 ** 33]
+    # powers of two, so that position * frequency is exact in f64 on both sides
+    case.inv = (2.0 ** -(np.arange(128) % 24)).astype(np.float32)
+    old_k, old_v = _caches(26, 8, "f32")
+    kd, vd = dev(old_k, "f32"), dev(old_v, "f32")
+    got = kca.attn_norm_rope_append(dev(case.q, "f32"), dev(case.k, "f32"), dev(case.v, "f32"), kd, vd, 0, **case.args())
+    # the kernel takes the angle in turns: one f64 product by 1 / 2 pi, off by
+    # 2^-53 (rounding) + 2^-53 (the constant) of up to 2^38 turns, 2 pi 2^-14 rad
+    want, length = case.want()
+    err = np.abs(widen(_host(got), "f32") - want[:, :8])
+    turns = np.abs(case.pos[0].astype(np.float64)) / (2 * np.pi)
+    bound = (2 * COMPUTE + 2 * np.pi * turns * 2.0 ** -51)[:, None, None] * length[:, :8] + 1e-30
+    assert float(np.max(err / bound)) <= 1.0
+
+
+def test_captured_step_on_another_stream_follows_device_positions():
+    """norm + rotation + append, then attn_decode_dev over the cache they fill,
+    captured once and replayed with new positions, lengths and inputs."""
+    batch, cap = 3, 200
+    old_k, old_v = _caches(28, batch * cap, "bf16")
+    kd, vd = dev(old_k, "bf16"), dev(old_v, "bf16")
+    first = Case(29, batch, "bf16")
+    q, k, v = (dev(x, "bf16") for x in (first.q, first.k, first.v))
+    pos = torch.zeros((1, batch), dtype=torch.int64, device="cuda")
+    dst = torch.zeros((batch,), dtype=torch.int64, device="cuda")
+    ctx = torch.ones((batch,), dtype=torch.int64, device="cuda")
+    inv = torch.from_numpy(first.inv).cuda()
+    q_out = torch.empty((batch, 8, 256), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((batch, 8, 256), dtype=torch.float32, device="cuda")
+    ws = kca.new_workspace(kca.attn_decode_workspace_bytes([cap] * batch))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        kca.attn_norm_rope_append(q, k, v, kd, vd, dst, pos, inv, q_out=q_out, workspace=ws, stream=stream)
+        kca.attn_decode_dev(q_out, kd.view(batch, cap, 256), vd.view(batch, cap, 256), ctx, cap, out=out, workspace=ws,
+                            stream=stream)
+
+    with torch.cuda.stream(stream):
+        dst.copy_(torch.arange(batch, device="cuda") * cap)
+        step()
+    stream.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for i, lens in enumerate(([1, 77, 200], [130, 2, 64])):
+        case = Case(30 + i, batch, "bf16", weights=False)
+        case.pos[0] = np.array(lens) - 1
+        for t, a in ((q, case.q), (k, case.k), (v, case.v)):
+            t.copy_(dev(a, "bf16"))
+        pos.copy_(torch.from_numpy(case.pos))
+        rows = np.arange(batch) * cap + case.pos[0]
+        dst.copy_(torch.from_numpy(rows))
+        ctx.copy_(torch.tensor(lens))
+        before = _host(kd).copy(), _host(vd).copy()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _check(case, q_out, "bf16", kd, vd, "bf16", *before, rows)
+        m, l, acc = decode_partial(_host(q_out), _host(kd).reshape(batch, cap, 256),
+                                   _host(vd).reshape(batch, cap, 256), lens, 0, q_dtype="bf16", kv_dtype="bf16")
+        assert max_err(out.cpu().numpy(), acc / l[..., None]) <= tol("bf16", "bf16")
+    assert kca.attn_device_status(ws)[0] == 0

@@ -1,0 +1,84 @@
+"""Host checks of attn_norm_rope_append that need no GPU, and pins of its
+oracle: refusals come back before any CUDA call, rotations keep lengths and
+relative positions, the norm is scale-free."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv_cache_attention_states_b200 as kca
+from oracle import norm_rope, rope
+
+P = 1 << 20   # never dereferenced: every call here is refused on the host
+
+
+def _call(**kw):
+    a = dict(q=P, q_stride=2048, k=P, k_stride=256, v=P, v_stride=256, in_dtype=kca.BF16, n_rows=4, flags=1, wq=P, wk=P,
+             w_dtype=kca.F32, w0=0.0, eps=1e-6, pos=P, n_axes=1, axis=None, inv=P, q_out=2 * P, q_out_dtype=kca.BF16,
+             kc=P, vc=P, kv_dtype=kca.BF16, cache_rows=100, dst=None, dst0=0, ws=None, stream=None)
+    assert not set(kw) - set(a)
+    a.update(kw)
+    return kca.lib().attn_norm_rope_append(*a.values())
+
+
+NULL, DTYPE, RANGE, ALIGN = -1, -3, -4, -6
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"q": None}, NULL), ({"k": None}, NULL), ({"v": None}, NULL), ({"q_out": None}, NULL), ({"kc": None}, NULL),
+    ({"vc": None}, NULL), ({"pos": None}, NULL), ({"inv": None}, NULL),
+    ({"in_dtype": 9}, DTYPE), ({"in_dtype": kca.I8}, DTYPE), ({"q_out_dtype": -1}, DTYPE), ({"kv_dtype": 7}, DTYPE),
+    ({"w_dtype": 5}, DTYPE),
+    ({"n_rows": 0}, RANGE), ({"n_rows": -1}, RANGE), ({"cache_rows": 0}, RANGE), ({"flags": 4}, RANGE),
+    ({"dst0": -1}, RANGE), ({"dst0": 97}, RANGE), ({"n_rows": 101}, RANGE), ({"eps": -1e-6}, RANGE),
+    ({"eps": float("nan")}, RANGE), ({"eps": float("inf")}, RANGE), ({"w0": float("nan")}, RANGE),
+    ({"n_axes": 0}, RANGE), ({"n_axes": 5}, RANGE),
+    ({"axis": (ctypes.c_uint8 * 128)(*([0] * 127 + [1]))}, RANGE),
+    ({"q": P, "q_out": P, "q_stride": 0}, RANGE), ({"q": P, "q_out": P, "q_out_dtype": kca.F16}, RANGE),
+    ({"q_stride": -8}, ALIGN), ({"q_stride": 2049}, ALIGN), ({"k_stride": 4}, ALIGN), ({"v_stride": (1 << 32) + 8}, ALIGN),
+    ({"q": P + 8}, ALIGN), ({"k": P + 2}, ALIGN), ({"v": P + 8}, ALIGN), ({"q_out": P + 4}, ALIGN),
+    ({"kc": P + 8}, ALIGN), ({"vc": P + 8}, ALIGN), ({"wq": P + 4}, ALIGN), ({"wk": P + 4}, ALIGN),
+    ({"inv": P + 4}, ALIGN), ({"pos": P + 4}, ALIGN), ({"dst": P + 4}, ALIGN), ({"ws": P + 2}, ALIGN),
+])
+def test_refusals(kw, code):
+    assert _call(**kw) == code
+
+
+def test_binding_refuses_cpu_tensors_and_bad_axes():
+    torch = pytest.importorskip("torch")
+    z = torch.zeros((2, 8, 256))
+    r = torch.zeros((2, 256))
+    with pytest.raises(ValueError):
+        kca.attn_norm_rope_append(z, r, r, r, r, 0)
+    for bad in ([0] * 127, [0] * 127 + [2], [0] * 129):
+        with pytest.raises(ValueError):
+            kca._freq_axis(bad, 2)
+
+
+def test_oracle_norm_is_scale_free_and_has_unit_mean_square():
+    x = np.random.default_rng(0).standard_normal((5, 256))
+    y = norm_rope.norm(x, eps=0.0)
+    assert np.allclose((y * y).mean(-1), 1.0, atol=1e-14)
+    assert np.allclose(norm_rope.norm(8 * x, eps=0.0), y, atol=1e-14)
+    w = np.random.default_rng(1).standard_normal(256)
+    assert np.allclose(norm_rope.norm(x, w, 1.0, 0.0), y * (1 + w), atol=1e-14)
+
+
+def test_oracle_rotation_depends_on_relative_position_and_matches_the_append():
+    rng = np.random.default_rng(2)
+    q, k = rng.standard_normal((2, 1, 1, 256))
+    inv = (1e4 ** (-np.arange(128) / 128.0)).astype(np.float32)
+    axis = [i % 3 for i in range(128)]
+
+    def dot(shift):
+        a, _ = norm_rope.turn(q, np.array([[9], [4], [2]]) + shift, inv, axis)
+        b, _ = norm_rope.turn(k, np.array([[3], [8], [1]]) + shift, inv, axis)
+        return float((a * b).sum())
+
+    assert abs(dot(0) - dot(1000)) < 1e-9
+    # one axis with the append's frequencies: the append's oracle, in f32 steps
+    cos, sin = rope.rope_tables([77])
+    want = rope.rope_rotate(k[0].astype(np.float32), cos, sin)
+    inv64 = 10000.0 ** (-np.arange(0, 128, dtype=np.float64) * 2.0 / 256)
+    got, _ = norm_rope.turn(k[0].astype(np.float32).astype(np.float64)[None], np.array([[77]]), inv64, [0] * 128)
+    assert np.abs(got[0] - want).max() < 2e-6
