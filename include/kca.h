@@ -463,6 +463,76 @@ int attn_norm_rope_append(const void *q, int64_t q_stride, const void *k_new, in
                           int64_t cache_rows, const int64_t *dst_rows_dev, int64_t dst_row0,
                           void *workspace, void *stream);
 
+/*
+ * Decode over selected blocks of keys.  A block is KCA_BLOCK_KEYS = 64
+ * consecutive positions from a multiple of 64 on; a sequence of ctx keys has
+ * ceil(ctx / 64) blocks, the last one possibly unfinished.  The pages have
+ * no counterpart to these calls.
+ *
+ * attn_summarize_blocks: bounds of the keys of every block that the newest
+ *   n_new positions of a sequence finished, i.e. of blocks j with
+ *   ctx - n_new < 64 (j + 1) <= ctx.  With hi / lo the largest / smallest value
+ *   of each dim over the block's 64 keys (NaN where one of them is):
+ *     scale = max(|hi|, |lo|) over the dims * f32(1/127)
+ *     codes = clamp(round_half_even(x / scale), -127, 127)  of hi, then of lo
+ *   (the quantisation of attn_quantize_k, one scale for the 512 values).
+ *   Summaries of other blocks are left as they are.
+ *     k_cache    [batch][capacity][256] kv_dtype, device
+ *     ctx_len_dev  DEVICE int64 [batch], 0..capacity, lengths after the append
+ *                (others are skipped and recorded: error bit 2)
+ *     n_new      1..capacity: a decode step gives 1, a prefill its rows
+ *     codes      int8 [batch][ceil(capacity/64)][2][256], device
+ *     scales     f32 [batch][ceil(capacity/64)], device
+ *     workspace  optional status word, or NULL
+ *
+ * attn_select_blocks: scores every block for the queries of a sequence and
+ *   lists the n_select best.  Score of block j, with the queries of the 8
+ *   heads quantised as in attn_decode_q8 (codes q8, scales sq):
+ *     s_j = max_h  f32(sum_t (q8 > 0 ? q8 * hi8_j : q8 * lo8_j)) * (sq_h * scale_j)
+ *   -- up to the quantisation an upper bound on any q.k of the block.  The
+ *   integer sum is exact and the products f32, so the choice is a function of
+ *   the inputs alone.  The first n_sink and the last n_recent of the
+ *   ceil(ctx/64) blocks are always taken (the last block's summary is not read
+ *   and need not exist), the others by score, NaN above all numbers, equal
+ *   scores by the lower index.
+ *     q          [batch][8][256] q_dtype
+ *     blocks_cap blocks per sequence of codes / scales, >= ceil(ctx_bound/64)-1
+ *     ctx_len_dev  DEVICE int64 [batch], each 0..ctx_bound (others: an empty
+ *                list, recorded); ctx_bound 1..131072
+ *     n_select   1..2048, n_sink >= 0, n_recent >= 1, n_sink + n_recent <= n_select
+ *     blocks     int32 [batch][n_select], device: the taken blocks in ascending
+ *                order, then -1
+ *     workspace  >= attn_select_blocks_workspace_bytes(batch, ctx_bound)
+ *
+ * attn_decode_blocks: attn_decode restricted to listed blocks: the query of
+ *   sequence b sees position p < ctx when block p / 64 is listed.
+ *     blocks     int32 [batch][n_list], device, n_list 1..2048, in any order;
+ *                -1 is skipped, any other entry outside 0..ceil(ctx/64)-1 is
+ *                skipped and recorded (error bit 5, value 16, detail
+ *                (17 << 24) | sequence).  A block listed twice counts twice.
+ *     ctx_len_dev, ctx_bound  as in attn_decode_dev
+ *     out        [batch][8][256] of out_dtype, which is F32 or q_dtype; a
+ *                sequence that sees no key gives zeros
+ *     workspace  >= attn_decode_blocks_workspace_bytes(batch, n_list)
+ *   There is no window.  Everything else is as in attn_decode.
+ */
+#define KCA_BLOCK_KEYS 64
+#define KCA_MAX_BLOCKS 2048
+int attn_summarize_blocks(const void *k_cache, int32_t kv_dtype, int64_t capacity, int32_t batch,
+                          const int64_t *ctx_len_dev, int64_t n_new, int8_t *codes, float *scales,
+                          void *workspace, void *stream);
+int attn_select_blocks(const void *q, int32_t q_dtype, const int8_t *codes, const float *scales,
+                       int64_t blocks_cap, int32_t batch, const int64_t *ctx_len_dev, int64_t ctx_bound,
+                       int32_t n_select, int32_t n_sink, int32_t n_recent, int32_t *blocks,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int attn_decode_blocks(const void *q, int32_t q_dtype, const void *k_cache, const void *v_cache,
+                       int32_t kv_dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                       int64_t capacity, int32_t batch, const int32_t *blocks, int32_t n_list,
+                       const int64_t *ctx_len_dev, int64_t ctx_bound, float scale, void *out,
+                       int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t attn_select_blocks_workspace_bytes(int32_t batch, int64_t ctx_bound);
+size_t attn_decode_blocks_workspace_bytes(int32_t batch, int32_t n_list);
+
 /* Workspace bytes the calls above need on the current device (0 on a bad
  * argument).  Always >= KCA_WORKSPACE_HEADER.  The size depends on the
  * device (its SM count sets the split plan), so it is asked of the device the
@@ -491,7 +561,8 @@ int attn_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
  * silently missing).
  * Error bits: 1 = a bounded wait ran out (detail: (site << 24) | block),
  * 2 = a device context length was out of range (detail: (10 << 24) | sequence),
- * 4 = an append destination was out of range (detail: (11 << 24) | row).
+ * 4 = an append destination was out of range (detail: (11 << 24) | row),
+ * 16 = a listed block was out of range (detail: (17 << 24) | sequence).
  * Returns KCA_OK when no kernel recorded an error since the last read,
  * KCA_ERR_DEVICE when one did (*detail, if not NULL, receives the record),
  * or KCA_ERR_CUDA when the copy itself failed.

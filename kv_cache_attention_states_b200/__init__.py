@@ -27,6 +27,7 @@ N_Q_HEADS, N_KV_HEADS, HEAD_DIM = 8, 1, 256
 MAX_CHUNK_ROWS, MAX_POSITION, MAX_BATCH, MAX_BATCH_ROWS = 768, 131072, 256, 15
 WORKSPACE_HEADER = 24832  # status word + per-(row, head) merge counters
 NORM_QK, NORM_V, MAX_ROPE_AXES = 1, 2, 4
+BLOCK_KEYS, MAX_BLOCKS = 64, 2048
 STATUS = {0: "KCA_OK", -1: "KCA_ERR_NULL", -2: "KCA_ERR_GEOMETRY", -3: "KCA_ERR_DTYPE",
           -4: "KCA_ERR_RANGE", -5: "KCA_ERR_WORKSPACE", -6: "KCA_ERR_ALIGN", -7: "KCA_ERR_CUDA",
           -8: "KCA_ERR_DEVICE"}
@@ -115,6 +116,17 @@ def load_library(path: str) -> ctypes.CDLL:
     L.attn_norm_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, f32, f32, vp, i32, vp,
                                         vp, vp, i32, vp, vp, i32, i64, vp, i64, vp, vp]
     L.attn_norm_rope_append.restype = ctypes.c_int
+    L.attn_summarize_blocks.argtypes = [vp, i32, i64, i32, vp, i64, vp, vp, vp, vp]
+    L.attn_summarize_blocks.restype = ctypes.c_int
+    L.attn_select_blocks.argtypes = [vp, i32, vp, vp, i64, i32, vp, i64, i32, i32, i32, vp, vp, sz, vp]
+    L.attn_select_blocks.restype = ctypes.c_int
+    L.attn_select_blocks_workspace_bytes.argtypes = [i32, i64]
+    L.attn_select_blocks_workspace_bytes.restype = sz
+    L.attn_decode_blocks.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i64, i32, vp, i32, vp, i64, f32, vp, i32,
+                                     vp, sz, vp]
+    L.attn_decode_blocks.restype = ctypes.c_int
+    L.attn_decode_blocks_workspace_bytes.argtypes = [i32, i32]
+    L.attn_decode_blocks_workspace_bytes.restype = sz
     L.attn_force_path.argtypes = [i32, i32]
     L.attn_force_path.restype = ctypes.c_int
     L.attn_status_string.argtypes = [ctypes.c_int]
@@ -558,6 +570,141 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
             _stream_ptr(stream, dev))
     _check(st, "attn_norm_rope_append")
     return q_out
+
+
+def _out_dtype(q, out, shape):
+    """`out`, or a new float32 tensor of `shape`, and its dtype code."""
+    import torch
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    if out.numel() != q.numel() or (out.dtype != torch.float32 and out.dtype != q.dtype):
+        raise ValueError("out must have q's shape and be float32 or of q's dtype")
+    return out, dtype_code(out)
+
+
+def _device_lengths(ctx_len_dev, batch: int):
+    import torch
+    if ctx_len_dev.dtype != torch.int64 or ctx_len_dev.numel() != batch:
+        raise ValueError("ctx_len_dev must be int64 with one entry per sequence")
+
+
+# ------------------------------------------------- decode over selected blocks
+
+def attn_summarize_blocks(k_cache, ctx_len_dev, n_new: int, codes=None, scales=None, workspace=None, stream=None):
+    """Bounds of the key blocks that the newest n_new positions finished.
+
+    k_cache: [batch, capacity, 256]; ctx_len_dev: int64 CUDA [batch], lengths
+    after the append; codes: int8 [batch, ceil(capacity / 64), 2, 256] and scales:
+    float32 [batch, ceil(capacity / 64)] (default: new and zero), in which the
+    other blocks stay as they are.  Returns codes, scales.
+    """
+    import torch
+    if not k_cache.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    batch, capacity, dev = k_cache.shape[0], k_cache.shape[1], k_cache.device
+    blocks = -(-capacity // BLOCK_KEYS)
+    if codes is None:
+        codes = torch.zeros((batch, blocks, 2, HEAD_DIM), dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.zeros((batch, blocks), dtype=torch.float32, device=dev)
+    _need(dev, k_cache=k_cache, ctx_len_dev=ctx_len_dev, codes=codes, scales=scales, workspace=workspace)
+    _device_lengths(ctx_len_dev, batch)
+    if k_cache.numel() != batch * capacity * HEAD_DIM:
+        raise ValueError("k_cache must be [batch, capacity, 256]")
+    if codes.dtype != torch.int8 or codes.numel() != batch * blocks * 2 * HEAD_DIM:
+        raise ValueError("codes must be int8 [batch, ceil(capacity / 64), 2, 256]")
+    if scales.dtype != torch.float32 or scales.numel() != batch * blocks:
+        raise ValueError("scales must be float32 [batch, ceil(capacity / 64)]")
+    with _on(dev):
+        st = lib().attn_summarize_blocks(k_cache.data_ptr(), dtype_code(k_cache), capacity, batch,
+                                         ctx_len_dev.data_ptr(), n_new, codes.data_ptr(), scales.data_ptr(),
+                                         _ptr(workspace), _stream_ptr(stream, dev))
+    _check(st, "attn_summarize_blocks")
+    return codes, scales
+
+
+def attn_select_blocks_workspace_bytes(batch: int, ctx_bound: int) -> int:
+    n = lib().attn_select_blocks_workspace_bytes(batch, ctx_bound)
+    if n == 0:
+        raise KcaError(-4, "attn_select_blocks_workspace_bytes")
+    return int(n)
+
+
+def attn_select_blocks(q, codes, scales, ctx_len_dev, ctx_bound: int, n_select: int, n_sink: int = 1,
+                       n_recent: int = 1, blocks=None, workspace=None, stream=None):
+    """The n_select best blocks of every sequence for its queries.
+
+    q: [batch, 8, 256]; codes / scales: the blocks' bounds (attn_summarize_blocks);
+    ctx_len_dev: int64 CUDA [batch], each 0..ctx_bound.  The first n_sink and the
+    last n_recent blocks are always taken.  Returns blocks int32
+    [batch, n_select], ascending, -1 behind the last.
+    """
+    import torch
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    batch, dev = q.shape[0], q.device
+    if blocks is None:
+        blocks = torch.empty((batch, n_select), dtype=torch.int32, device=dev)
+    _need(dev, q=q, codes=codes, scales=scales, ctx_len_dev=ctx_len_dev, blocks=blocks, workspace=workspace)
+    _device_lengths(ctx_len_dev, batch)
+    if q.numel() != batch * N_Q_HEADS * HEAD_DIM:
+        raise ValueError("q must be [batch, 8, 256]")
+    if (codes.dtype != torch.int8 or scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != batch
+            or codes.numel() != scales.numel() * 2 * HEAD_DIM):
+        raise ValueError("codes must be int8 [batch, blocks, 2, 256] and scales float32 [batch, blocks]")
+    if blocks.dtype != torch.int32 or blocks.numel() != batch * n_select:
+        raise ValueError("blocks must be int32 [batch, n_select]")
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(attn_select_blocks_workspace_bytes(batch, ctx_bound), dev, stream)
+        st = lib().attn_select_blocks(q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), scales.shape[1],
+                                      batch, ctx_len_dev.data_ptr(), ctx_bound, n_select, n_sink, n_recent,
+                                      blocks.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                      _stream_ptr(stream, dev))
+    _check(st, "attn_select_blocks")
+    return blocks
+
+
+def attn_decode_blocks_workspace_bytes(batch: int, n_list: int) -> int:
+    n = lib().attn_decode_blocks_workspace_bytes(batch, n_list)
+    if n == 0:
+        raise KcaError(-4, "attn_decode_blocks_workspace_bytes")
+    return int(n)
+
+
+def attn_decode_blocks(q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound: int, scale: float = 1.0 / 16.0, out=None,
+                       workspace=None, stream=None):
+    """Decode restricted to listed blocks of 64 keys.
+
+    q: [batch, 8, 256]; k_cache / v_cache: [batch, capacity, 256]; blocks: int32
+    CUDA [batch, n_list] in any order, -1 skipped; ctx_len_dev: int64 CUDA
+    [batch], each 0..ctx_bound; out: float32 (the default) or of q's dtype.
+    Returns out [batch, 8, 256].
+    """
+    import torch
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    batch, dev = q.shape[0], q.device
+    _need(dev, q=q, k_cache=k_cache, v_cache=v_cache, blocks=blocks, ctx_len_dev=ctx_len_dev, out=out,
+          workspace=workspace)
+    _device_lengths(ctx_len_dev, batch)
+    if k_cache.shape[0] != batch or v_cache.shape != k_cache.shape or q.numel() != batch * N_Q_HEADS * HEAD_DIM:
+        raise ValueError("q, k_cache and v_cache must agree in batch and shape")
+    if k_cache.dtype != v_cache.dtype:
+        raise TypeError("k_cache and v_cache must share a dtype")
+    if blocks.dtype != torch.int32 or blocks.dim() != 2 or blocks.shape[0] != batch:
+        raise ValueError("blocks must be int32 [batch, n_list]")
+    out, od = _out_dtype(q, out, (batch, N_Q_HEADS, HEAD_DIM))
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(attn_decode_blocks_workspace_bytes(batch, blocks.shape[1]), dev, stream)
+        st = lib().attn_decode_blocks(q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
+                                      dtype_code(k_cache), N_Q_HEADS, N_KV_HEADS, HEAD_DIM, k_cache.shape[1], batch,
+                                      blocks.data_ptr(), blocks.shape[1], ctx_len_dev.data_ptr(), ctx_bound, scale,
+                                      out.data_ptr(), od, workspace.data_ptr(), workspace.numel(),
+                                      _stream_ptr(stream, dev))
+    _check(st, "attn_decode_blocks")
+    return out
 
 
 # ------------------------------------------------------- quantised-dot decode

@@ -1060,6 +1060,80 @@ int attn_decode_q8(const void* q, int32_t q_dtype, const void* k8_cache, const v
   return kca::launch_rows_q8(q_dtype, v_dtype, (sane & 1) != 0, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
 }
 
+// Lists of n_list blocks: every sequence's list is planned as n_list whole
+// blocks of keys (the lists themselves are on the device).
+size_t attn_decode_blocks_workspace_bytes(int32_t batch, int32_t n_list) {
+  if (batch < 1 || batch > KCA_MAX_BATCH || n_list < 1 || n_list > KCA_MAX_BLOCKS) return 0;
+  int sms = 0;
+  if (current_sms(&sms) != KCA_OK) return 0;
+  int64_t nk[KCA_MAX_BATCH];
+  for (int32_t b = 0; b < batch; ++b) nk[b] = (int64_t)n_list * KCA_BLOCK_KEYS;
+  return rows_ws_bytes_any(batch, nk, sms);
+}
+
+int attn_decode_blocks(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache, int32_t kv_dtype,
+                       int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t capacity, int32_t batch,
+                       const int32_t* blocks, int32_t n_list, const int64_t* ctx_len_dev, int64_t ctx_bound,
+                       float scale, void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  if (!q || !k_cache || !v_cache || !out || !workspace || !blocks || !ctx_len_dev) return KCA_ERR_NULL;
+  int st = geometry_status(n_q_heads, n_kv_heads, head_dim);
+  if (st != KCA_OK) return st;
+  if (!dtype_ok(q_dtype) || !dtype_ok(kv_dtype) || (out_dtype != KCA_F32 && out_dtype != q_dtype)) return KCA_ERR_DTYPE;
+  if (capacity < 1 || capacity > KCA_MAX_POSITION || batch < 1 || batch > KCA_MAX_BATCH || ctx_bound < 0 ||
+      ctx_bound > capacity || n_list < 1 || n_list > KCA_MAX_BLOCKS || !std::isfinite(scale) || !(scale > 0.f))
+    return KCA_ERR_RANGE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(ctx_len_dev) % 8) != 0 || (reinterpret_cast<uintptr_t>(blocks) % 4) != 0)
+    return KCA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0) return KCA_ERR_WORKSPACE;
+  int sms = 0;
+  if (current_sms(&sms) != KCA_OK) return KCA_ERR_CUDA;
+  int64_t nk[KCA_MAX_BATCH];
+  for (int32_t b = 0; b < batch; ++b) nk[b] = (int64_t)n_list * KCA_BLOCK_KEYS;
+  int cluster = 1;
+  kca::RowsPlan p;
+  if (workspace_bytes < rows_ws_bytes_any(batch, nk, sms, &p, &cluster)) return KCA_ERR_WORKSPACE;
+  const bool mma = kv_dtype != KCA_F32;   // one kernel per cache type here, whatever attn_force_path pins
+  if (mma && cluster < 1) return KCA_ERR_CUDA;
+  if (!mma) p = kca::make_rows_plan(batch, nk, sms);
+  kca::RowsArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.out = static_cast<float*>(out);
+  a.out_dtype = out_dtype;
+  a.status = workspace;
+  a.seq_rows = capacity;
+  a.n_units = batch;
+  a.split_len = p.split_len;
+  a.max_splits = p.max_splits;
+  a.scale = scale;
+  a.ctx_dev = ctx_len_dev;
+  a.ctx_bound = ctx_bound;
+  a.blocks = blocks;
+  a.n_list = n_list;
+  a.cache_rows = (int64_t)batch * capacity;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!mma) {
+    a.part_slots = a.max_splits > 1 ? (int64_t)a.n_units * a.max_splits : 0;
+    carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc);
+    return kca::launch_rows_blocks(q_dtype, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+  }
+  a.cluster = cluster;
+  a.max_clusters = (a.max_splits + cluster - 1) / cluster;
+  a.part_slots = a.max_clusters > 1 ? (int64_t)a.n_units * a.max_clusters : 0;
+  if (a.max_clusters > 1) {
+    a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kStatusBytes);
+    carve(workspace, (size_t)a.n_units * a.max_clusters * kHeads * 2 * 4, &a.cpart_ml, &a.cpart_acc);
+  }
+  CUtensorMap tmk, tmv;
+  if (!encode_kv_map(&tmk, k_cache, kv_dtype, 0, a.cache_rows, 64) ||
+      !encode_kv_map(&tmv, v_cache, kv_dtype, 0, a.cache_rows, 64))
+    return KCA_ERR_CUDA;
+  return kca::launch_decode_mma_blocks(q_dtype, kv_dtype, tmk, tmv, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+}
+
 int attn_merge_partials(int32_t n_parts, int32_t batch, const float* parts, int64_t part_stride, float* out,
                         void* stream) {
   if (!parts || !out) return KCA_ERR_NULL;

@@ -78,6 +78,15 @@ struct DBars {
   float ro[8][256];
 };
 constexpr int kDSmemBytes = kDOffBar + (int)sizeof(DBars) + 1024;
+// Block variant: the split's block indices, 16 bits each, behind the barriers.
+constexpr int kDOffIds = kDOffBar + (int)sizeof(DBars);
+constexpr int kDBlkSmemBytes = kDSmemBytes + KCA_MAX_BLOCKS * 2;
+static_assert(kDStageKeys == KCA_BLOCK_KEYS, "a stage of the block variant is one block");
+static_assert(kDBlkSmemBytes <= 232448, "shared memory over the per-CTA limit");
+// f16 probabilities of the block variant are kept 2^7 larger (at most 2^15
+// under the lazy rescale), so that those far below the reference stay normal
+// numbers; l carries the same factor and the quotient loses it.
+constexpr float kDBlkShift = 7.f;
 
 template <int KT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -213,7 +222,7 @@ __device__ __forceinline__ void st_peer2(float* local, uint32_t cta, float v0, f
 // partials.  NB partials per batch of loads (the smallest batch that holds
 // all of them, up to 32 / W; loads past nclus repeat partial 0 and are
 // weighted 0).  Every thread of the block calls this (it holds a bar.sync).
-template <int W, int NB>
+template <bool BLK, int W, int NB>
 __device__ __forceinline__ void merge_cluster_partials(const RowsArgs& a, float* sm_m, float* sm_l, int64_t u0,
                                                        int unit, int rank, int C, int nh, int d, int nclus,
                                                        int lane) {
@@ -276,27 +285,31 @@ __device__ __forceinline__ void merge_cluster_partials(const RowsArgs& a, float*
     if (c0 + NB >= nclus) break;
     load_batch(c0 + NB);
   }
-  float* dst = a.out + ((int64_t)unit * kHeads + h) * kDim + W * jd;
+  const int64_t o0 = ((int64_t)unit * kHeads + h) * kDim + W * jd;
 #pragma unroll
-  for (int e = 0; e < W; ++e) dst[e] = rows_final(a, acc[e], M, L);
+  for (int e = 0; e < W; ++e) rows_store<BLK>(a, o0 + e, rows_final(a, acc[e], M, L));
   if (jd == 0) rows_write_ml(a, unit, h, M, L);
 }
 
-template <int W>
+template <bool BLK, int W>
 __device__ __forceinline__ void merge_cluster_partials_nb(const RowsArgs& a, float* sm_m, float* sm_l, int64_t u0,
                                                           int unit, int rank, int C, int nh, int d, int nclus,
                                                           int lane) {
-  if (nclus <= 4) merge_cluster_partials<W, 4>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-  else if (nclus <= 8) merge_cluster_partials<W, 8>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-  else if (W > 1 || nclus <= 16) merge_cluster_partials<W, 16>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-  else merge_cluster_partials<W, 32>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+  if (nclus <= 4) merge_cluster_partials<BLK, W, 4>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+  else if (nclus <= 8) merge_cluster_partials<BLK, W, 8>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+  else if (W > 1 || nclus <= 16) merge_cluster_partials<BLK, W, 16>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+  else merge_cluster_partials<BLK, W, 32>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
 }
 
 // KT: K element type, or KCA_I8 for packed int8 K rows (the quantised-dot
 // variant: QK on int8 codes with exact int32 MMA, scaled by the query's and
 // the key's scales); VT: V element type (16-bit); tms: the int8 rows' scale
-// column (unused otherwise).
-template <int QT, int KT, int VT = KT>
+// column (unused otherwise).  BLK: attention over listed blocks (16-bit K):
+// a stage is one block, fetched from wherever its list entry points, its keys
+// past the context masked; splits are runs of list entries.  A template
+// argument because the list costs a barrier and dependent loads before the
+// first stage that the range form does not need.
+template <int QT, int KT, int VT = KT, bool BLK = false>
 __global__ void __launch_bounds__(kDThreads, 1)
     decode_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tms, const RowsArgs a) {
@@ -318,12 +331,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
   const int lane = threadIdx.x & 31;
   // Device context lengths may come from the previous kernel of the stream:
   // with them, the dependency wait comes before they are read.
-  if (a.ctx_dev != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
-  int64_t seq_base;
-  const int64_t pos = rows_unit_pos(a, unit, split == 0 && threadIdx.x == 0, &seq_base);
-  int64_t lo;
-  const int64_t nkeys = rows_keys(a, pos, &lo);
-  const int32_t split_len = rows_split_len(a, nkeys, kDStageKeys);
+  // (The block variant's plan does not depend on them: it reads them later.)
+  if (!BLK && a.ctx_dev != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+  int64_t seq_base = (int64_t)unit * a.seq_rows;
+  int64_t pos = 0, lo = 0;
+  if (!BLK) pos = rows_unit_pos(a, unit, split == 0 && threadIdx.x == 0, &seq_base);
+  const int64_t nkeys = BLK ? (int64_t)a.n_list * kDStageKeys : rows_keys(a, pos, &lo);
+  const int32_t split_len = BLK ? a.split_len : rows_split_len(a, nkeys, kDStageKeys);
   const int32_t nsplit = rows_n_splits(nkeys, split_len);
   const int nclus = (nsplit + C - 1) / C;
   if (clus >= nclus) return;               // the whole cluster leaves together
@@ -342,8 +356,9 @@ __global__ void __launch_bounds__(kDThreads, 1)
                                          unit < KCA_MAX_CHUNK_ROWS)),
                      status, kSiteBoundsDecode, (unsigned)unit))
     return;
-  if (active && !KCA_IN_BOUNDS(base_row + kbeg >= 0 && base_row + kend <= a.cache_rows, status,
-                               kSiteBoundsDecode, (unsigned)unit))
+  if (active && !KCA_IN_BOUNDS(BLK ? seq_base + a.seq_rows <= a.cache_rows
+                                   : base_row + kbeg >= 0 && base_row + kend <= a.cache_rows,
+                               status, kSiteBoundsDecode, (unsigned)unit))
     active = false;
   const int n_stage = active ? (int)cdiv(kend - kbeg, kDStageKeys) : 0;
 
@@ -367,7 +382,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
     if (kQ8) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tms)) : "memory");
-    if (active) {
+    if (!BLK && active) {
       int64_t n = kend - kbeg;
       if (n > kDPrefetchKeys) n = kDPrefetchKeys;
       constexpr int kKRow = kQ8 ? KCA_I8_ROW_BYTES : kDim * 2;
@@ -390,6 +405,16 @@ __global__ void __launch_bounds__(kDThreads, 1)
 
   const int nh = kHeads / C;               // heads each CTA owns in the merge
 
+  // Block variant: the sequence's length and the split's list entries, once.
+  short* ids = reinterpret_cast<short*>(smem + kDOffIds);
+  int64_t ctx = 0;
+  if constexpr (BLK) {
+    ctx = rows_ctx(a, unit, split == 0 && threadIdx.x == 0);
+    const int e0 = (int)(kbeg / kDStageKeys);
+    for (int i = threadIdx.x; i < n_stage; i += kDThreads) ids[i] = (short)rows_block(a, unit, e0 + i, ctx);
+    __syncthreads();
+  }
+
   if (warp == kDWarps) {
     // ---------------------------------------------------------------- producer
     if (lane == 0 && active) {
@@ -401,7 +426,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
           break;
         const uint32_t kst = sbase + slot * kDStageBytes;
         const uint32_t bar = smem_u32(&bars->full[slot]);
-        const int32_t row0 = (int32_t)(base_row + kbeg + (int64_t)i * kDStageKeys);
+        const int32_t row0 = BLK ? (int32_t)(seq_base + (int64_t)ids[i] * kDStageKeys)
+                                 : (int32_t)(base_row + kbeg + (int64_t)i * kDStageKeys);
+        if (BLK && ids[i] < 0) {   // no block: an empty stage
+          mbar_arrive(&bars->full[slot]);
+          issued = i + 1;
+          continue;
+        }
         if constexpr (kQ8) {
           mbar_arrive_expect_tx(&bars->full[slot], kDQ8StageTx);
           tma2d(kst, &tmk, 0, row0, bar);                  // codes 0..127
@@ -511,8 +542,15 @@ __global__ void __launch_bounds__(kDThreads, 1)
       const int slot = i % kDStages;
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars->full[slot], (i / kDStages) & 1, abort_flag,
                                                    status, kSiteRowsFull));
-      const int64_t k0 = kbeg + (int64_t)i * kDStageKeys;
-      const int cnt = (int)((kend - k0) < kDStageKeys ? (kend - k0) : kDStageKeys);
+      // keys of the stage: up to the split's end, or a block's up to the context
+      const int64_t left = BLK ? (ids[i] < 0 ? 0 : ctx - (int64_t)ids[i] * kDStageKeys)
+                               : kend - (kbeg + (int64_t)i * kDStageKeys);
+      const int cnt = (int)(left < kDStageKeys ? left : kDStageKeys);
+      if (BLK && cnt <= 0) {   // an empty stage (the same for every warp)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->empty[slot]);
+        continue;
+      }
       const uint32_t kst = sbase + slot * kDStageBytes;
       const uint32_t vst = kst + kDHalfBytes;
       float sx0 = -INFINITY, sx1 = -INFINITY;
@@ -524,6 +562,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
             *reinterpret_cast<uint4*>(vrows + (u >> 3) * kDBoxBytes + row * 128 + (u & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
+          // a block's stage may be followed by a TMA write of the same slot
+          if (BLK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         const int kr = 8 * warp + (lane & 7);
         const int kk0 = 8 * warp + 2 * tig;
@@ -582,8 +622,9 @@ __global__ void __launch_bounds__(kDThreads, 1)
             for (int j = 0; j < 4; ++j) o[nt][j] *= alpha;
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        const float p0 = exp2f((sx0 - mu) * kDLog2e);
-        const float p1 = exp2f((sx1 - mu) * kDLog2e);
+        constexpr float kShift = BLK && VT == KCA_F16 ? kDBlkShift : 0.f;
+        const float p0 = exp2f((sx0 - mu) * kDLog2e + kShift);
+        const float p1 = exp2f((sx1 - mu) * kDLog2e + kShift);
         l_part += p0 + p1;
         const uint32_t hi = pack16<VT>(p0, p1);
         const float2 f = unpack16<VT>(hi);
@@ -686,7 +727,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         }
       }
       if (nclus == 1) {
-        a.out[((int64_t)unit * kHeads + h) * kDim + d] = rows_final(a, O, M, L);
+        rows_store<BLK>(a, ((int64_t)unit * kHeads + h) * kDim + d, rows_final(a, O, M, L));
         if (d == 0) rows_write_ml(a, unit, h, M, L);
         continue;
       }
@@ -722,32 +763,33 @@ __global__ void __launch_bounds__(kDThreads, 1)
         float* sm_m = reinterpret_cast<float*>(smem);          // [8][256]
         float* sm_l = sm_m + kHeads * kDim;                    // [8][256]
         const int64_t u0 = (int64_t)unit * a.max_clusters * kHeads;   // cluster 0, head 0
-        if (nh == 1) merge_cluster_partials_nb<1>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-        else if (nh == 2) merge_cluster_partials_nb<2>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-        else if (nh == 4) merge_cluster_partials_nb<4>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
-        else merge_cluster_partials_nb<8>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+        if (nh == 1) merge_cluster_partials_nb<BLK, 1>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+        else if (nh == 2) merge_cluster_partials_nb<BLK, 2>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+        else if (nh == 4) merge_cluster_partials_nb<BLK, 4>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
+        else merge_cluster_partials_nb<BLK, 8>(a, sm_m, sm_l, u0, unit, rank, C, nh, d, nclus, lane);
         if (d == 0) a.tickets[unit * kHeads + rank] = 0;   // ready for the next call
       }
     }
   }
 }
 
-template <int QT, int KT, int VT = KT>
+template <int QT, int KT, int VT = KT, bool BLK = false>
 cudaError_t launch_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tms, const RowsArgs& a,
                      cudaStream_t stream) {
-  auto kern = decode_mma_kernel<QT, KT, VT>;
+  auto kern = decode_mma_kernel<QT, KT, VT, BLK>;
+  constexpr int smem = BLK ? kDBlkSmemBytes : kDSmemBytes;
   static std::atomic<bool> attr_set[64];   // per device; zero-initialised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.max_clusters * a.cluster, a.n_units, 1);
   cfg.blockDim = dim3(kDThreads, 1, 1);
-  cfg.dynamicSmemBytes = kDSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   int na = 0;
@@ -1208,6 +1250,21 @@ cudaError_t launch_decode_mma(int q_dtype, int kv_dtype, const CUtensorMap& tmk,
   KCA_DMMA_CASE(KCA_BF16, KCA_F16)
   KCA_DMMA_CASE(KCA_BF16, KCA_BF16)
 #undef KCA_DMMA_CASE
+  return e;
+}
+
+cudaError_t launch_decode_mma_blocks(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                     const RowsArgs& a, cudaStream_t stream) {
+  cudaError_t e = cudaErrorInvalidValue;
+#define KCA_DBLK_CASE(QD, KD) \
+  if (q_dtype == QD && kv_dtype == KD) e = launch_t<QD, KD, KD, true>(tmk, tmv, tmk, a, stream);
+  KCA_DBLK_CASE(KCA_F32, KCA_F16)
+  KCA_DBLK_CASE(KCA_F32, KCA_BF16)
+  KCA_DBLK_CASE(KCA_F16, KCA_F16)
+  KCA_DBLK_CASE(KCA_F16, KCA_BF16)
+  KCA_DBLK_CASE(KCA_BF16, KCA_F16)
+  KCA_DBLK_CASE(KCA_BF16, KCA_BF16)
+#undef KCA_DBLK_CASE
   return e;
 }
 

@@ -92,7 +92,10 @@ __device__ __forceinline__ uint32_t q8_code(float x, float sx) {
   return static_cast<uint32_t>(c) & 0xffu;
 }
 
-template <int QT, int KT, int VT = KT, bool DP4A = true>
+// BLK: attention over listed blocks of 64 keys (kca_rows.h): "key" p of a
+// split is key p % 64 of list entry p / 64, so a stage of 16 keys stays inside
+// one block.
+template <int QT, int KT, int VT = KT, bool DP4A = true, bool BLK = false>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a) {
   using S = RowsSmem<KT, VT>;
   constexpr bool kQ8 = KT == KCA_I8;
@@ -107,11 +110,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  int64_t seq_base;
-  const int64_t pos = rows_unit_pos(a, unit, split == 0 && threadIdx.x == 0, &seq_base);
-  int64_t lo;
-  const int64_t nkeys = rows_keys(a, pos, &lo);
-  const int32_t split_len = rows_split_len(a, nkeys, kRowsSplitQuantum);
+  int64_t seq_base = (int64_t)unit * a.seq_rows;
+  int64_t lo = 0, ctx = 0, nkeys;
+  if constexpr (BLK) {
+    ctx = rows_ctx(a, unit, split == 0 && threadIdx.x == 0);
+    nkeys = (int64_t)a.n_list * KCA_BLOCK_KEYS;
+  } else {
+    const int64_t pos = rows_unit_pos(a, unit, split == 0 && threadIdx.x == 0, &seq_base);
+    nkeys = rows_keys(a, pos, &lo);
+  }
+  const int32_t split_len = BLK ? a.split_len : rows_split_len(a, nkeys, kRowsSplitQuantum);
   const int32_t nsplit = rows_n_splits(nkeys, split_len);
   if (split >= nsplit) return;
   const int64_t kbeg = lo + (int64_t)split * split_len;
@@ -122,7 +130,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
   float* out = a.out + (int64_t)unit * kHeads * kDim;
   // bounds-checked builds: the split's rows lie in the cache and its partial
   // slot in the workspace (no CTA of this kernel waits on another)
-  if (!KCA_IN_BOUNDS(nsplit <= a.max_splits && base_row + kbeg >= 0 && base_row + kend <= a.cache_rows &&
+  if (!KCA_IN_BOUNDS(nsplit <= a.max_splits &&
+                         (BLK ? seq_base + a.seq_rows <= a.cache_rows
+                              : base_row + kbeg >= 0 && base_row + kend <= a.cache_rows) &&
                          (nsplit == 1 || (int64_t)(unit + 1) * a.max_splits <= a.part_slots),
                      status, kSiteBoundsRows, (unsigned)unit))
     return;
@@ -134,6 +144,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
     return;
   }
   const int n_stage = (int)cdiv(kend - kbeg, kKeysPerStage);
+  // Keys of stage i, the first at cache row *row.
+  auto stage_keys = [&](int i, int64_t* row) -> int {
+    const int64_t k0 = kbeg + (int64_t)i * kKeysPerStage;
+    int64_t left = kend - k0;
+    *row = base_row + k0;
+    if constexpr (BLK) {
+      const int64_t id = rows_block(a, unit, (int)(k0 / KCA_BLOCK_KEYS), ctx);
+      const int64_t p = id * KCA_BLOCK_KEYS + k0 % KCA_BLOCK_KEYS;   // position of the stage's first key
+      left = id < 0 || p >= ctx ? 0 : ctx - p;
+      *row = seq_base + p;
+    }
+    return (int)(left < kKeysPerStage ? left : kKeysPerStage);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -157,14 +180,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
         if (i >= kStages &&
             !mbar_wait(&empty[slot], ((i / kStages) - 1) & 1, abort_flag, status, kSiteRowsEmpty))
           break;
-        const int64_t k0 = kbeg + (int64_t)i * kKeysPerStage;
-        const int cnt = (int)((kend - k0) < kKeysPerStage ? (kend - k0) : kKeysPerStage);
+        int64_t row0;
+        const int cnt = stage_keys(i, &row0);
+        if (BLK && cnt == 0) {   // no block, or past the context: an empty stage
+          mbar_arrive(&full[slot]);
+          issued = i + 1;
+          continue;
+        }
         const uint32_t kbytes = (uint32_t)cnt * S::kKRowBytes;
         const uint32_t vbytes = (uint32_t)cnt * S::kVRowBytes;
         unsigned char* dst = smem + slot * S::kStageBytes;
         mbar_arrive_expect_tx(&full[slot], kbytes + vbytes);
-        bulk_g2s(dst, kg + (base_row + k0) * S::kKRowBytes, kbytes, &full[slot]);
-        bulk_g2s(dst + kKeysPerStage * S::kKRowBytes, vg + (base_row + k0) * S::kVRowBytes, vbytes,
+        bulk_g2s(dst, kg + row0 * S::kKRowBytes, kbytes, &full[slot]);
+        bulk_g2s(dst + kKeysPerStage * S::kKRowBytes, vg + row0 * S::kVRowBytes, vbytes,
                  &full[slot]);
         issued = i + 1;
       }
@@ -226,8 +254,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
       ok = __all_sync(0xffffffffu,
                       mbar_wait(&full[slot], (i / kStages) & 1, abort_flag, status, kSiteRowsFull));
       if (!ok) break;
-      const int64_t k0 = kbeg + (int64_t)i * kKeysPerStage;
-      const int cnt = (int)((kend - k0) < kKeysPerStage ? (kend - k0) : kKeysPerStage);
+      int64_t row0;
+      const int cnt = stage_keys(i, &row0);
       const unsigned char* st = smem + slot * S::kStageBytes;
       const int nk = (warp < cnt ? 1 : 0) + (warp + kComputeWarps < cnt ? 1 : 0);
       if (nk > 0) {
@@ -342,7 +370,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
         A[0] += f * x0.x; A[1] += f * x0.y; A[2] += f * x0.z; A[3] += f * x0.w;
         A[4] += f * x1.x; A[5] += f * x1.y; A[6] += f * x1.z; A[7] += f * x1.w;
       }
-      if (nsplit == 1) {
+      if (BLK && nsplit == 1) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          rows_store<BLK>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, rows_final(a, A[t], M, L));
+      } else if (nsplit == 1) {
         const float inv = a.out_ml != nullptr ? 1.f : 1.f / L;
         float4* o = reinterpret_cast<float4*>(out + h * kDim + 8 * lane);
         o[0] = make_float4(A[0] * inv, A[1] * inv, A[2] * inv, A[3] * inv);
@@ -363,9 +395,27 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
 }
 
 // Log-sum-exp merge of the splits of each unit: one CTA per (unit, head),
-// its eight warps taking interleaved splits.
+// its eight warps taking interleaved splits.  BLK: the block variant's splits
+// and output type (the merged row passes through shared memory).
+template <bool BLK>
 __global__ void __launch_bounds__(256) merge_rows_kernel(const RowsArgs a) {
   const int unit = blockIdx.x >> 3, h = blockIdx.x & 7;
+  if constexpr (BLK) {
+    const int32_t ns = rows_n_splits((int64_t)a.n_list * KCA_BLOCK_KEYS, a.split_len);
+    if (!KCA_IN_BOUNDS(ns <= a.max_splits && (int64_t)(unit + 1) * a.max_splits <= a.part_slots,
+                       static_cast<DeviceStatus*>(a.status), kSiteBoundsMerge, (unsigned)unit))
+      return;
+    __shared__ float redb[8 * 264];
+    __shared__ __align__(16) float row[kDim];
+    const int64_t r0 = (int64_t)unit * a.max_splits * kHeads + h;
+    const int lane = threadIdx.x & 31;
+    merge_row<8>(ns, a.part_ml + r0 * 2, kHeads * 2, a.part_acc + r0 * kDim, kHeads * kDim, kLog2e, row, redb,
+                 threadIdx.x >> 5, lane, 1);
+    if (threadIdx.x < 32)   // the group's first warp wrote the row, each lane its own dims
+      for (int t = 0; t < 8; ++t)
+        rows_store<BLK>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, row[8 * lane + t]);
+    return;
+  }
   int64_t seq_base;
   const int64_t pos = rows_unit_pos(a, unit, false, &seq_base);
   int64_t lo;
@@ -382,10 +432,10 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const RowsArgs a) {
                threadIdx.x & 31, 1, a.out_ml != nullptr ? a.out_ml + ((int64_t)unit * kHeads + h) * 2 : nullptr);
 }
 
-template <int QT, int KT, int VT = KT, bool DP4A = true>
+template <int QT, int KT, int VT = KT, bool DP4A = true, bool BLK = false>
 cudaError_t launch_rows_t(const RowsArgs& a, cudaStream_t stream) {
   using S = RowsSmem<KT, VT>;
-  auto kern = rows_kernel<QT, KT, VT, DP4A>;
+  auto kern = rows_kernel<QT, KT, VT, DP4A, BLK>;
   static std::atomic<bool> attr_set[64];   // per device; zero-initialised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -399,14 +449,23 @@ cudaError_t launch_rows_t(const RowsArgs& a, cudaStream_t stream) {
   kern<<<grid, kRowsThreads, S::kTotal, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.max_splits <= 1) return e;
-  return launch_merge_rows(a, stream);
+  if (!BLK) return launch_merge_rows(a, stream);
+  merge_rows_kernel<true><<<a.n_units * kHeads, 256, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_merge_rows(const RowsArgs& a, cudaStream_t stream) {
-  merge_rows_kernel<<<a.n_units * kHeads, 256, 0, stream>>>(a);
+  merge_rows_kernel<false><<<a.n_units * kHeads, 256, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rows_blocks(int q_dtype, const RowsArgs& a, cudaStream_t stream) {
+  if (q_dtype == KCA_F32) return launch_rows_t<KCA_F32, KCA_F32, KCA_F32, true, true>(a, stream);
+  if (q_dtype == KCA_F16) return launch_rows_t<KCA_F16, KCA_F32, KCA_F32, true, true>(a, stream);
+  if (q_dtype == KCA_BF16) return launch_rows_t<KCA_BF16, KCA_F32, KCA_F32, true, true>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_rows(int q_dtype, int kv_dtype, const RowsArgs& a, cudaStream_t stream) {

@@ -55,6 +55,13 @@ struct RowsArgs {
   int64_t cache_rows;
   int64_t part_slots;
   int64_t ctx[KCA_MAX_BATCH];  // decode: ctx_len per sequence
+  // Block lists (the kernels' block variants; attn_decode_blocks): unit u
+  // attends to the blocks of 64 keys at blocks[u * n_list ..] (-1: none)
+  // instead of a key range, "key" p of its splits being key p % 64 of list
+  // entry p / 64; out is of out_dtype.
+  const int32_t* blocks;
+  int32_t n_list;
+  int32_t out_dtype;
 };
 
 // Rows of one unit of the batched multi-row kernels: 4 (both kernels), or 8
@@ -109,6 +116,22 @@ __device__ __forceinline__ float rows_final(const RowsArgs& a, float acc, float 
   if (a.out_ml != nullptr) return acc;
   return (M == -INFINITY && L == 0.f) ? 0.f : acc / L;
 }
+// Block variants: entry i of unit's list as a block index whose first key the
+// sequence has (ctx: its length), or -1; anything else listed is recorded.
+__device__ __forceinline__ int rows_block(const RowsArgs& a, int unit, int i, int64_t ctx) {
+  const int32_t id = a.blocks[(int64_t)unit * a.n_list + i];
+  if (id >= 0 && (int64_t)id * KCA_BLOCK_KEYS < ctx) return id;
+  if (id != -1) record_error(static_cast<DeviceStatus*>(a.status), kSiteBlock, kErrBadBlock, (unsigned)unit);
+  return -1;
+}
+// One output value at element idx of out: f32, or with the block variants of
+// out_dtype (rounded once, to nearest even).
+template <bool BLK>
+__device__ __forceinline__ void rows_store(const RowsArgs& a, int64_t idx, float v) {
+  if (BLK && a.out_dtype == KCA_F16) reinterpret_cast<__half*>(a.out)[idx] = __float2half_rn(v);
+  else if (BLK && a.out_dtype == KCA_BF16) reinterpret_cast<__nv_bfloat16*>(a.out)[idx] = __float2bfloat16_rn(v);
+  else a.out[idx] = v;
+}
 // Unit u of a batched call in multi-row units (a.unit_rows rows each):
 // sequence *b, first row *i0 (of the sequence's rows), *nr rows; positions
 // ctx[b] - rows_per_seq + i0 + r.
@@ -133,6 +156,9 @@ __device__ __forceinline__ void multirow_unit(const RowsArgs& a, int u, int* b, 
 #endif
 
 cudaError_t launch_rows(int q_dtype, int kv_dtype, const RowsArgs& a, cudaStream_t stream);
+
+// The block variant for f32 caches (a.blocks set; a.ctx_dev gives the lengths).
+cudaError_t launch_rows_blocks(int q_dtype, const RowsArgs& a, cudaStream_t stream);
 
 // The CUDA-core rows kernel with packed int8 K rows (KCA_I8) and V of
 // v_dtype: the quantised-dot variant; dp4a selects the instruction over its
@@ -203,5 +229,8 @@ int decode_mma_cluster_capacity(int c);
 // the same kernel (clusters + tickets).
 cudaError_t launch_decode_mma(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
                               const RowsArgs& a, cudaStream_t stream);
+// The same over listed blocks (a.blocks set; a.ctx_dev gives the lengths).
+cudaError_t launch_decode_mma_blocks(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                     const RowsArgs& a, cudaStream_t stream);
 
 }  // namespace kca

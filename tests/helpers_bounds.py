@@ -1,0 +1,31 @@
+"""Error bounds of the f32-grade attention kernels, derived from their
+arithmetic: what a computed output may differ from the exact one by."""
+import numpy as np
+
+HALF_STEP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def f32_grade(q_dtype, kv_dtype, absqk, vmax, n_parts=4):
+    """absqk [...]: the largest scale * sum |q||k| of a key of the row; vmax: the
+    largest |v| it sees.  Per unit of |v|:
+
+    scores: the query is held as two parts of the cache's type (2^-22 for f16,
+    2^-16 for bf16, exact when it is of the cache's type or the cache is f32);
+    a dot product of 256 takes at most 16 dependent accumulations, each off by
+    2 ulp of 2^-23 at most, and 3 more roundings (scale, sums): 2^-18.  An error
+    e of every score moves the output by at most 2 e |v|.
+    probabilities: two 16-bit parts (f16: 2^-22, bf16: 2^-16), the exponent's
+    argument (|s| log2 e rounded at 2^-24 of up to absqk: counted with the
+    scores) and exp2f (2 ulp): 2^-16 covers them.
+    sums: accumulation in f32, at most 2^-18 for stages merged in n_parts or
+    more partials, each merge 4 roundings of 2^-24."""
+    uq = 0.0 if q_dtype == kv_dtype or kv_dtype == "f32" else (2.0 ** -22 if kv_dtype == "f16" else 2.0 ** -16)
+    up = {"f32": 2.0 ** -22, "f16": 2.0 ** -20, "bf16": 2.0 ** -15}[kv_dtype]
+    e = 2 * np.asarray(absqk) * (uq + 2.0 ** -18) + up + 2.0 ** -18
+    return e * vmax
+
+
+def rounded(want, bound, out_dtype):
+    """bound plus the rounding of the output to its type (half a step; f16
+    subnormals 2^-25)."""
+    return bound + HALF_STEP[out_dtype] * (np.abs(want) + bound) + (2.0 ** -25 if out_dtype == "f16" else 1e-38)

@@ -1,0 +1,357 @@
+"""GPU parity of the block calls -- bounds of finished blocks
+(attn_summarize_blocks), the choice of blocks (attn_select_blocks) and decode
+over them (attn_decode_blocks) -- against the f64 oracle: codes and lists bit
+for bit, outputs within the bound of their arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_attention_states_b200 as kca
+from kv_cache_attention_states_b200 import synth
+from oracle import blocks as ob
+from tests.helpers import dev
+from tests.helpers_bounds import f32_grade, rounded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup(cuda_ok):
+    kca.lib()
+
+
+def _i64(x):
+    return torch.tensor(np.asarray(x, dtype=np.int64), device="cuda")
+
+
+def _keys(seed, batch, cap, kv, std=1.0):
+    drift = np.repeat(synth.normal(seed, "d", (batch, -(-cap // 64), 256), 0.5), 64, 1)[:, :cap]
+    return synth.to_storage(synth.normal(seed, "k", (batch, cap, 256), std) + drift, kv)
+
+
+# ------------------------------------------------------------------ summaries
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cap,n_new", [(64, 64), (64, 1), (300, 1), (300, 65), (1024, 1024), (1000, 130), (63, 63)])
+def test_summaries_are_exact_and_leave_other_blocks(kv, cap, n_new):
+    ctx = sorted({c for c in (0, 1, 63, 64, 65, 127, 128, 129, 192, cap - 1, cap) if 0 <= c <= cap})
+    k = _keys(1, len(ctx), cap, kv)
+    nb = -(-cap // 64)
+    codes = synth.integers(2, "c", -127, 127, len(ctx) * nb * 512).astype(np.int8).reshape(len(ctx), nb, 2, 256)
+    scales = synth.normal(2, "s", (len(ctx), nb))
+    c, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    got = kca.attn_summarize_blocks(dev(k, kv), _i64(ctx), n_new, codes=c, scales=s)
+    assert got[0] is c and got[1] is s
+    wc, wsc = ob.summarize(k, kv, ctx, n_new, codes, scales)
+    assert np.array_equal(c.cpu().numpy(), wc) and np.array_equal(s.cpu().numpy(), wsc)
+
+
+@pytest.mark.parametrize("kv", ["f16", "f32"])
+def test_summaries_of_odd_values_and_bad_lengths(kv):
+    cap = 320
+    k = _keys(3, 3, cap, kv)
+    k[0, 10, 5] = np.inf          # block 0: an infinite scale, codes 0
+    k[0, 70, 9] = np.nan          # block 1: NaN scale, codes 0
+    k[0, 128:192] = 0             # block 2: scale 0
+    k[0, 200] = np.float32(6e-8)  # a subnormal f16
+    ctx = [320, 321, -1]
+    ws = kca.new_workspace(kca.WORKSPACE_HEADER)
+    c, s = kca.attn_summarize_blocks(dev(k, kv), _i64(ctx), cap, workspace=ws)
+    z = np.zeros((3, 5, 2, 256), np.int8), np.zeros((3, 5), np.float32)
+    wc, wsc = ob.summarize(k, kv, ctx, cap, *z)
+    assert np.array_equal(c.cpu().numpy(), wc) and np.array_equal(s.cpu().numpy(), wsc, equal_nan=True)
+    assert not c[1:].any() and not s[1:].any()
+    st, detail = kca.attn_device_status(ws)
+    assert st == -8 and detail >> 24 == 10 and detail & 0xFFFFFF in (1, 2)
+
+
+# ------------------------------------------------------------------ selection
+
+def _summ(seed, batch, cap, kv="f16"):
+    k = _keys(seed, batch, cap, kv)
+    nb = -(-cap // 64)
+    return ob.summarize(k, kv, [cap // 64 * 64] * batch, cap, np.zeros((batch, nb, 2, 256), np.int8),
+                        np.zeros((batch, nb), np.float32))
+
+
+def _select(q, qd, codes, scales, ctx, bound, n, sink=1, recent=1, **kw):
+    got = kca.attn_select_blocks(dev(q, qd), torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(),
+                                 _i64(ctx), bound, n, sink, recent, **kw)
+    return got.cpu().numpy()
+
+
+def _want(q, qd, codes, scales, ctx, n, sink=1, recent=1):
+    return np.array([ob.select(q[b], qd, codes[b], scales[b], ctx[b], n, sink, recent) for b in range(len(ctx))],
+                    dtype=np.int32)
+
+
+@pytest.mark.parametrize("qd", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n,sink,recent", [(1, 0, 1), (2, 1, 1), (9, 3, 4), (64, 1, 1), (65, 0, 2), (200, 1, 1)])
+def test_select_lists_are_exact(qd, n, sink, recent):
+    cap = 8128 + 37
+    ctx = [0, 1, 64, 65, 129, 4096, 4097, 8128, cap, 640, 6001]
+    codes, scales = _summ(5, len(ctx), cap)
+    q = synth.draw(6, "q", (len(ctx), 8, 256), qd)
+    assert np.array_equal(_select(q, qd, codes, scales, ctx, cap, n, sink, recent),
+                          _want(q, qd, codes, scales, ctx, n, sink, recent))
+
+
+@pytest.mark.parametrize("n", [2, 17, 64, 2000, 2048])
+def test_select_over_the_longest_context(n):
+    cap = 131072
+    rng = np.random.default_rng(7)
+    codes = rng.integers(-127, 128, (2, 2048, 2, 256), dtype=np.int8)
+    scales = rng.random((2, 2048), dtype=np.float32)
+    ctx = [131072, 131072 - 64 * 700 - 5]
+    q = synth.draw(7, "q", (2, 8, 256), "f32")
+    assert np.array_equal(_select(q, "f32", codes, scales, ctx, cap, n), _want(q, "f32", codes, scales, ctx, n))
+
+
+@pytest.mark.parametrize("n", [2, 3, 30, 99])
+def test_select_ties_go_to_the_lower_index(n):
+    cap = 64 * 150
+    codes, scales = _summ(8, 4, cap)
+    codes[0, 20:], scales[0, 20:] = codes[0, 3], scales[0, 3]        # 130 equal blocks
+    codes[1, :], scales[1, :] = codes[1, 0], scales[1, 0]            # all equal
+    q = synth.draw(8, "q", (4, 8, 256), "f16")
+    q[2] = 0                                                         # every score 0
+    scales[3, ::2] = 0                                               # zeros among positive and negative scores
+    ctx = [cap, cap - 1, cap, cap]
+    assert np.array_equal(_select(q, "f16", codes, scales, ctx, cap, n), _want(q, "f16", codes, scales, ctx, n))
+
+
+def test_select_puts_nan_first_and_infinite_scales_too():
+    cap = 64 * 100
+    codes, scales = _summ(9, 3, cap)
+    scales[0, 40], codes[0, 40] = np.nan, 0
+    scales[1, 41], codes[1, 41] = np.inf, 0
+    q = synth.draw(9, "q", (3, 8, 256), "f32")
+    q[2, 3, 7] = np.nan                                              # a NaN head: every score NaN
+    ctx = [cap] * 3
+    got = _select(q, "f32", codes, scales, ctx, cap, 3)
+    assert 40 in got[0] and 41 in got[1]
+    assert np.array_equal(got, _want(q, "f32", codes, scales, ctx, 3))
+
+
+def test_select_needs_no_summary_of_the_last_block_and_records_bad_lengths():
+    bound = 64 * 65 + 3
+    codes, scales = _summ(10, 4, 64 * 65)                            # blocks_cap = ceil(bound / 64) - 1
+    assert scales.shape[1] == 65
+    q = synth.draw(10, "q", (4, 8, 256), "bf16")
+    ctx = [bound, bound + 1, -5, 64 * 65]
+    ws = kca.new_workspace(kca.attn_select_blocks_workspace_bytes(4, bound))
+    got = _select(q, "bf16", codes, scales, ctx, bound, 7, workspace=ws)
+    want = _want(q, "bf16", codes, scales, [bound, 0, 0, 64 * 65], 7)
+    assert np.array_equal(got, want)
+    st, detail = kca.attn_device_status(ws)
+    assert st == -8 and detail >> 24 == 10 and detail & 0xFFFFFF in (1, 2)
+    assert np.array_equal(_select(q, "bf16", codes, scales, [bound] * 4, bound, 7, workspace=ws),
+                          _want(q, "bf16", codes, scales, [bound] * 4, 7))   # the tickets are ready again
+
+
+# ------------------------------------------------------------------- attention
+
+def _data(seed, batch, cap, qd, kv, std=1.0):
+    return (synth.draw(seed, "q", (batch, 8, 256), qd), _keys(seed, batch, cap, kv, std),
+            synth.draw(seed, "v", (batch, cap, 256), kv))
+
+
+def _check_out(got, out_dt, q, qd, k, v, kv, lists, ctx):
+    got = got.float().cpu().numpy().astype(np.float64)
+    for b in range(len(ctx)):
+        want, absqk, vmax = ob.attend(q[b], qd, k[b], v[b], kv, lists[b], ctx[b])
+        bound = rounded(want, f32_grade(qd, kv, absqk, vmax)[:, None], out_dt)
+        worst = float(np.max(np.abs(got[b] - want) / bound))
+        assert worst <= 1.0, (b, worst)
+
+
+PAIRS = [("f16", "f16", "f16"), ("bf16", "bf16", "bf16"), ("f32", "f16", "f32"), ("f32", "bf16", "f32"),
+         ("f16", "bf16", "f32"), ("bf16", "f16", "f32"), ("f32", "f32", "f32"), ("f16", "f32", "f16"),
+         ("bf16", "f32", "f32")]
+
+
+@pytest.mark.parametrize("qd,kv,od", PAIRS)
+@pytest.mark.parametrize("n_list", [1, 3, 21, 64])
+def test_decode_blocks_matches_oracle(qd, kv, od, n_list):
+    """Shuffled lists with holes; keys and values of blocks that are not listed,
+    and of rows past the context, are poison."""
+    cap = 64 * 40 + 13
+    ctx = [cap, 64 * 17, 64 * 9 + 1, 63, 1, 0, 2000]
+    batch = len(ctx)
+    q, k, v = _data(20, batch, cap, qd, kv)
+    rng = np.random.default_rng(n_list)
+    lists = np.full((batch, n_list), -1, dtype=np.int32)
+    for b, c in enumerate(ctx):
+        nb = -(-c // 64)
+        ids = rng.permutation(nb)[:n_list]
+        lists[b, rng.permutation(n_list)[:len(ids)]] = ids
+    kp, vp = dev(k, kv), dev(v, kv)
+    for b, c in enumerate(ctx):
+        seen = torch.zeros(cap, dtype=torch.bool)
+        for j in lists[b]:
+            if j >= 0:
+                seen[64 * j:min(64 * (j + 1), c)] = True
+        kp[b, ~seen.cuda()] = float("nan")
+        vp[b, ~seen.cuda()] = float("inf")
+    out = torch.full((batch, 8, 256), 9.0, dtype=synth.torch_dtype(od), device="cuda")
+    ws = kca.new_workspace(kca.attn_decode_blocks_workspace_bytes(batch, n_list))
+    got = kca.attn_decode_blocks(dev(q, qd), kp, vp, torch.from_numpy(lists).cuda(), _i64(ctx), cap, out=out,
+                                 workspace=ws)
+    assert got is out
+    _check_out(got, od, q, qd, k, v, kv, lists, ctx)
+    assert bool((out[ctx.index(0)] == 0).all())
+    assert kca.attn_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("kv", ["f16", "f32"])
+def test_long_lists_split_over_the_gpu(kv):
+    cap = 131072 if kv == "f16" else 70000
+    q, k, v = _data(21, 1, cap, "f32", kv)
+    ctx = [cap - 5]
+    n = -(-cap // 64)
+    lists = np.random.default_rng(1).permutation(n).astype(np.int32)[None]
+    got = kca.attn_decode_blocks(dev(q, "f32"), dev(k, kv), dev(v, kv), torch.from_numpy(lists).cuda(), _i64(ctx), cap)
+    _check_out(got, "f32", q, "f32", k, v, kv, lists, ctx)
+    plain = kca.attn_decode_dev(dev(q, "f32"), dev(k, kv), dev(v, kv), _i64(ctx), cap)
+    assert float((got - plain).abs().max()) <= 1e-4    # all blocks listed: the whole context
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "f32"])
+def test_many_sequences_and_large_scores(kv):
+    """256 sequences; scores of hundreds, so that one key takes nearly all."""
+    batch, cap, n = 256, 320, 4
+    q, k, v = _data(22, batch, cap, "f32", kv, std=6.0)
+    ctx = [int(c) for c in synth.integers(22, "ctx", 1, cap, batch)]
+    lists = np.array([(list(np.random.default_rng(b).permutation(-(-c // 64))[:n]) + [-1] * n)[:n]
+                      for b, c in enumerate(ctx)], dtype=np.int32)
+    got = kca.attn_decode_blocks(dev(q, "f32"), dev(k, kv), dev(v, kv), torch.from_numpy(lists).cuda(), _i64(ctx), cap)
+    _check_out(got, "f32", q, "f32", k, v, kv, lists, ctx)
+
+
+@pytest.mark.parametrize("kv", ["f16", "f32"])
+def test_bad_entries_are_skipped_and_recorded(kv):
+    cap = 64 * 12
+    ctx = [500, 700]
+    q, k, v = _data(23, 2, cap, "f32", kv)
+    lists = np.array([[3, 8, 1 << 30, 0], [10, 11, -2, -1]], dtype=np.int32)   # 500 keys: blocks 0..7; 700: 0..10
+    ws = kca.new_workspace(kca.attn_decode_blocks_workspace_bytes(2, 4))
+    got = kca.attn_decode_blocks(dev(q, "f32"), dev(k, kv), dev(v, kv), torch.from_numpy(lists).cuda(), _i64(ctx), cap,
+                                 workspace=ws)
+    _check_out(got, "f32", q, "f32", k, v, kv, [[3, 0], [10]], ctx)
+    st, detail = kca.attn_device_status(ws)
+    assert st == -8 and detail >> 24 == 17 and detail & 0xFFFFFF in (0, 1)
+    ctx = [cap + 1, -1]
+    got = kca.attn_decode_blocks(dev(q, "f32"), dev(k, kv), dev(v, kv),
+                                 torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), _i64(ctx), cap, workspace=ws)
+    assert bool((got == 0).all())
+    st, detail = kca.attn_device_status(ws)
+    assert st == -8 and detail >> 24 == 10
+
+
+@pytest.mark.parametrize("kv", ["f16", "f32"])
+def test_a_block_listed_twice_counts_twice(kv):
+    q, k, v = _data(24, 1, 192, "f32", kv)
+    lists = np.array([[2, 0, 2]], dtype=np.int32)
+    got = kca.attn_decode_blocks(dev(q, "f32"), dev(k, kv), dev(v, kv), torch.from_numpy(lists).cuda(), _i64([150]), 192)
+    _check_out(got, "f32", q, "f32", k, v, kv, lists, [150])
+
+
+@pytest.mark.parametrize("qd,kv", [("bf16", "bf16"), ("f32", "f32")])
+def test_captured_step_of_all_calls_on_another_stream(qd, kv):
+    """append, bounds, choice and attention captured once, replayed as the
+    sequences grow; the lists and outputs follow the device's lengths."""
+    batch, cap, n = 3, 64 * 9, 3
+    q, k, v = _data(25, batch, cap, qd, kv)
+    kd, vd = torch.zeros_like(dev(k, kv)), torch.zeros_like(dev(v, kv))
+    start = [255, 130, 511]
+    for b, c in enumerate(start):
+        kd[b, :c], vd[b, :c] = dev(k, kv)[b, :c], dev(v, kv)[b, :c]
+    ctx = _i64(start)
+    codes, scales = kca.attn_summarize_blocks(kd, ctx, cap)
+    qt = dev(q, qd)
+    new_k, new_v = torch.empty((batch, 256), device="cuda"), torch.empty((batch, 256), device="cuda")
+    dst = torch.zeros(batch, dtype=torch.int64, device="cuda")
+    blocks = torch.empty((batch, n), dtype=torch.int32, device="cuda")
+    out = torch.empty((batch, 8, 256), dtype=torch.float32, device="cuda")
+    ws = kca.new_workspace(max(kca.attn_select_blocks_workspace_bytes(batch, cap),
+                               kca.attn_decode_blocks_workspace_bytes(batch, n)))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        kca.attn_append_kv(new_k, new_v, kd.view(-1, 256), vd.view(-1, 256), dst, workspace=ws, stream=stream)
+        kca.attn_summarize_blocks(kd, ctx, 1, codes=codes, scales=scales, workspace=ws, stream=stream)
+        kca.attn_select_blocks(qt, codes, scales, ctx, cap, n, blocks=blocks, workspace=ws, stream=stream)
+        kca.attn_decode_blocks(qt, kd, vd, blocks, ctx, cap, out=out, workspace=ws, stream=stream)
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for t in range(3):
+        lens = [c + t + 1 for c in start]
+        for b, c in enumerate(lens):
+            new_k[b], new_v[b] = dev(k, kv)[b, c - 1].float(), dev(v, kv)[b, c - 1].float()
+        ctx.copy_(_i64(lens))
+        dst.copy_(_i64([b * cap + c - 1 for b, c in enumerate(lens)]))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        wc, wsc = ob.summarize(k, kv, lens, cap, np.zeros((batch, 9, 2, 256), np.int8), np.zeros((batch, 9), np.float32))
+        assert np.array_equal(codes.cpu().numpy(), wc) and np.array_equal(scales.cpu().numpy(), wsc)
+        lists = _want(q, qd, wc, wsc, lens, n)
+        assert np.array_equal(blocks.cpu().numpy(), lists)
+        _check_out(out, "f32", q, qd, k, v, kv, lists, lens)
+    assert kca.attn_device_status(ws)[0] == 0
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    batch, cap, n = 5, 64 * 60, 20
+    data = [_data(26 + i, batch, cap, "f16", "f16") for i in range(2)]
+    ctx = [cap, 700, 3000, 64, 129]
+    wants, outs = [], [[], []]
+    tens = []
+    for i, (q, k, v) in enumerate(data):
+        c, s = _summ(26 + i, batch, cap)
+        lists = _want(q, "f16", c, s, ctx, n)
+        wants.append(lists)
+        tens.append((dev(q, "f16"), dev(k, "f16"), dev(v, "f16"), torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda(),
+                     _i64(ctx), kca.new_workspace(kca.attn_select_blocks_workspace_bytes(batch, cap)),
+                     kca.new_workspace(kca.attn_decode_blocks_workspace_bytes(batch, n))))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            q, k, v, c, s, cd, w1, w2 = tens[i]
+            with torch.cuda.stream(st):
+                bl = kca.attn_select_blocks(q, c, s, cd, cap, n, workspace=w1, stream=st)
+                outs[i].append((bl, kca.attn_decode_blocks(q, k, v, bl, cd, cap, workspace=w2, stream=st)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for bl, o in outs[i]:
+            assert np.array_equal(bl.cpu().numpy(), wants[i])
+            assert torch.equal(o, outs[i][0][1])
+        _check_out(outs[i][0][1], "f32", data[i][0], "f16", data[i][1], data[i][2], "f16", wants[i], ctx)
+
+
+@pytest.mark.parametrize("kv,n_list", [("f16", 64), ("bf16", 3), ("f32", 40)])
+def test_decode_blocks_through_the_checked_build(kv, n_list):
+    """The bounds-checked build records nothing and gives the same bits."""
+    cap = 64 * 50 + 9
+    ctx = [cap, 1000, 1]
+    q, k, v = _data(29, 3, cap, "f32", kv)
+    lists = torch.from_numpy(np.random.default_rng(3).integers(-1, 16, (3, n_list)).astype(np.int32)).cuda()
+    lists[2] = 0
+    args = dev(q, "f32"), dev(k, kv), dev(v, kv), lists, _i64(ctx), cap
+    ws = kca.new_workspace(kca.attn_decode_blocks_workspace_bytes(3, n_list))
+    a = kca.attn_decode_blocks(*args, workspace=ws)
+    torch.cuda.synchronize()
+    saved = kca._lib
+    kca._lib = kca.load_library(kca.LIB_CHECKED_PATH)
+    try:
+        b = kca.attn_decode_blocks(*args, workspace=ws)
+        torch.cuda.synchronize()
+        assert kca.attn_device_status(ws)[0] == 0
+    finally:
+        kca._lib = saved
+    assert torch.equal(a, b)
