@@ -464,6 +464,50 @@ int attn_norm_rope_append(const void *q, int64_t q_stride, const void *k_new, in
                           void *workspace, void *stream);
 
 /*
+ * attn_decode_prefix -- decode of a batch whose sequences share a long prefix
+ * (one document, one system prompt): the prefix's K/V exist once and are read
+ * once for the whole batch, each sequence's own keys as in attn_decode.  The
+ * pages have no counterpart to this call.
+ *   prefix_k/prefix_v  rows of positions 0..prefix_len-1, [prefix_len][256]
+ *                kv_dtype, device (may be NULL when prefix_len is 0)
+ *   prefix_len   0..131072
+ *   k_cache/v_cache  [batch][capacity][1][256] kv_dtype: row r of sequence b
+ *                holds position prefix_len + r
+ *   ctx_len      HOST int64 [batch]: whole context lengths, each in
+ *                prefix_len..prefix_len+capacity and <= 131072; the query of
+ *                sequence b sits at ctx_len[b]-1.  Or NULL, and
+ *   ctx_len_dev  DEVICE int64 [batch] with the host bound ctx_bound on every
+ *                value, read when the kernels run (as in attn_decode_dev, so
+ *                that one captured launch serves every step).  A value outside
+ *                prefix_len..ctx_bound is never used as an address: its row is
+ *                computed as an empty context (zeros) and recorded (error bit
+ *                2, detail (10 << 24) | sequence).  Give exactly one of the two.
+ *   window, scale  as in attn_decode: positions [ctx-window, ctx-1] are seen
+ *   out          [batch][8][256] of out_dtype, which is F32 or q_dtype
+ *   workspace    >= attn_decode_prefix_workspace_bytes(...) bytes; with
+ *                ctx_len_dev, ask for ctx_len = {ctx_bound, ...}
+ * q_dtype == kv_dtype in {F16, BF16} and 3 or more sequences take the
+ * tensor-core prefill kernel for the prefix, whose probabilities are rounded to
+ * kv_dtype before the V product (as in attn_prefill: the relative error of a
+ * 16-bit rounding, whatever out_dtype).  Other 16-bit caches take multi-row
+ * units, f32 caches and single sequences the decode kernels, all f32-grade; the
+ * sequences' own keys take the kernels of attn_decode_partial.  With a 16-bit
+ * cache and 2 or more sequences, V must be finite on the prefix rows from
+ * prefix_len - window (0 without a window) on: a masked key's probability is 0,
+ * and 0 times an infinity is not.
+ * A sequence that sees no key gives zeros.
+ * Everything else is as in attn_decode.
+ */
+int attn_decode_prefix(const void *q, int32_t q_dtype, const void *prefix_k, const void *prefix_v,
+                       int64_t prefix_len, const void *k_cache, const void *v_cache, int32_t kv_dtype,
+                       int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t capacity,
+                       int32_t batch, const int64_t *ctx_len, const int64_t *ctx_len_dev,
+                       int64_t ctx_bound, int32_t window, float scale, void *out, int32_t out_dtype,
+                       void *workspace, size_t workspace_bytes, void *stream);
+size_t attn_decode_prefix_workspace_bytes(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len,
+                                          int32_t batch, const int64_t *ctx_len, int32_t window);
+
+/*
  * Decode over selected blocks of keys.  A block is KCA_BLOCK_KEYS = 64
  * consecutive positions from a multiple of 64 on; a sequence of ctx keys has
  * ceil(ctx / 64) blocks, the last one possibly unfinished.  The pages have

@@ -116,6 +116,11 @@ def load_library(path: str) -> ctypes.CDLL:
     L.attn_norm_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, f32, f32, vp, i32, vp,
                                         vp, vp, i32, vp, vp, i32, i64, vp, i64, vp, vp]
     L.attn_norm_rope_append.restype = ctypes.c_int
+    L.attn_decode_prefix.argtypes = [vp, i32, vp, vp, i64, vp, vp, i32, i32, i32, i32, i64, i32, p64, vp, i64, i32,
+                                     f32, vp, i32, vp, sz, vp]
+    L.attn_decode_prefix.restype = ctypes.c_int
+    L.attn_decode_prefix_workspace_bytes.argtypes = [i32, i32, i64, i32, p64, i32]
+    L.attn_decode_prefix_workspace_bytes.restype = sz
     L.attn_summarize_blocks.argtypes = [vp, i32, i64, i32, vp, i64, vp, vp, vp, vp]
     L.attn_summarize_blocks.restype = ctypes.c_int
     L.attn_select_blocks.argtypes = [vp, i32, vp, vp, i64, i32, vp, i64, i32, i32, i32, vp, vp, sz, vp]
@@ -572,6 +577,8 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
     return q_out
 
 
+# ------------------------------------------------------ shared-prefix decode
+
 def _out_dtype(q, out, shape):
     """`out`, or a new float32 tensor of `shape`, and its dtype code."""
     import torch
@@ -586,6 +593,68 @@ def _device_lengths(ctx_len_dev, batch: int):
     import torch
     if ctx_len_dev.dtype != torch.int64 or ctx_len_dev.numel() != batch:
         raise ValueError("ctx_len_dev must be int64 with one entry per sequence")
+
+
+def attn_decode_prefix_workspace_bytes(q_dtype: int, kv_dtype: int, prefix_len: int, ctx_len, window: int = 0) -> int:
+    """Workspace of attn_decode_prefix (with device lengths: ask for
+    [ctx_bound] * batch)."""
+    nctx, ptr = _i64_array(ctx_len)
+    n = lib().attn_decode_prefix_workspace_bytes(q_dtype, kv_dtype, prefix_len, nctx, ptr, window)
+    if n == 0:
+        raise KcaError(-4, "attn_decode_prefix_workspace_bytes")
+    return int(n)
+
+
+def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache, ctx_len, window: int = 0,
+                       scale: float = 1.0 / 16.0, ctx_bound: int | None = None, out=None, workspace=None, stream=None):
+    """Decode of sequences that share a prefix, whose K/V exist and are read once.
+
+    q: [batch, 8, 256]; prefix_k / prefix_v: [>= prefix_len, 256] (None when
+    prefix_len is 0); k_cache / v_cache: [batch, capacity, 256], row r of a
+    sequence holding position prefix_len + r; ctx_len: whole context lengths, as
+    host ints or as an int64 CUDA tensor with the host bound ctx_bound; out:
+    float32 (the default) or of q's dtype.  Returns out [batch, 8, 256].
+    """
+    import torch
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    batch, dev = q.shape[0], q.device
+    on_device = isinstance(ctx_len, torch.Tensor) and ctx_len.is_cuda
+    _need(dev, q=q, prefix_k=prefix_k, prefix_v=prefix_v, k_cache=k_cache, v_cache=v_cache, out=out,
+          workspace=workspace, ctx_len=ctx_len if on_device else None)
+    if k_cache.shape[0] != batch or v_cache.shape != k_cache.shape or q.numel() != batch * N_Q_HEADS * HEAD_DIM:
+        raise ValueError("q, k_cache and v_cache must agree in batch and shape")
+    if prefix_len > 0 and (prefix_k is None or prefix_v is None):
+        raise ValueError("a prefix of more than 0 rows needs prefix_k and prefix_v")
+    for t in (prefix_k, prefix_v, v_cache):
+        if t is not None and t.dtype != k_cache.dtype:
+            raise TypeError("the prefix and the caches must share a dtype")
+    for t in (prefix_k, prefix_v):
+        if t is not None and t.numel() < prefix_len * HEAD_DIM:
+            raise ValueError("the prefix has fewer than prefix_len rows")
+    capacity = k_cache.shape[1]
+    out, od = _out_dtype(q, out, (batch, N_Q_HEADS, HEAD_DIM))
+    qd, kd = dtype_code(q), dtype_code(k_cache)
+    if on_device:
+        _device_lengths(ctx_len, batch)
+        if ctx_bound is None:
+            ctx_bound = min(prefix_len + capacity, MAX_POSITION)
+        host_p, dev_p = None, ctx_len.data_ptr()
+    else:
+        nctx, host_p = _i64_array(ctx_len)
+        if nctx != batch:
+            raise ValueError("ctx_len must have one entry per sequence")
+        dev_p, ctx_bound = None, 0
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(attn_decode_prefix_workspace_bytes(
+                qd, kd, prefix_len, [ctx_bound] * batch if on_device else ctx_len, window), dev, stream)
+        st = lib().attn_decode_prefix(q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(),
+                                      v_cache.data_ptr(), kd, N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p,
+                                      dev_p, ctx_bound, window, scale, out.data_ptr(), od, workspace.data_ptr(),
+                                      workspace.numel(), _stream_ptr(stream, dev))
+    _check(st, "attn_decode_prefix")
+    return out
 
 
 # ------------------------------------------------- decode over selected blocks

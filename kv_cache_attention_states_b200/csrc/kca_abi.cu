@@ -261,8 +261,8 @@ bool encode_rows_map(CUtensorMap* m, const void* base, int32_t dtype, int64_t ro
   return encode_2d(m, t, base, dims, (cuuint64_t)kDim * esz, box);
 }
 
-void carve(void* ws, size_t ml_bytes, float** ml, float** acc) {
-  char* p = static_cast<char*>(ws) + KCA_WORKSPACE_HEADER;
+void carve(void* ws, size_t ml_bytes, float** ml, float** acc, size_t offset = KCA_WORKSPACE_HEADER) {
+  char* p = static_cast<char*>(ws) + offset;
   *ml = reinterpret_cast<float*>(p);
   *acc = reinterpret_cast<float*>(p + align_up(ml_bytes));
 }
@@ -374,9 +374,11 @@ kca::RowsPlan rows_plan(int32_t kv_dtype, int32_t n_units, const int64_t* nkeys,
 }
 
 // Launches the rows path: tensor cores for 16-bit caches (tensor maps over the
-// cache_rows rows of the cache), CUDA cores otherwise.
+// cache_rows rows of the cache), CUDA cores otherwise.  offset: where the
+// partials start in the workspace.
 int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, const void* v_cache,
-                     int64_t cache_rows, kca::RowsArgs a, int cluster, void* workspace, cudaStream_t s) {
+                     int64_t cache_rows, kca::RowsArgs a, int cluster, void* workspace, cudaStream_t s,
+                     size_t offset = KCA_WORKSPACE_HEADER) {
   a.cache_rows = cache_rows;
   if (use_rows_mma(kv_dtype)) {
     a.cluster = cluster;
@@ -386,7 +388,7 @@ int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, con
       // Counters live in the header (no other path writes there), cluster
       // partials where the CUDA-core path keeps its split partials.
       a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kStatusBytes);
-      carve(workspace, (size_t)a.n_units * a.max_clusters * kHeads * 2 * 4, &a.cpart_ml, &a.cpart_acc);
+      carve(workspace, (size_t)a.n_units * a.max_clusters * kHeads * 2 * 4, &a.cpart_ml, &a.cpart_acc, offset);
     }
     CUtensorMap tmk, tmv;
     if (!encode_kv_map(&tmk, k_cache, kv_dtype, 0, cache_rows, 64) ||
@@ -395,7 +397,7 @@ int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, con
     return kca::launch_decode_mma(q_dtype, kv_dtype, tmk, tmv, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
   }
   a.part_slots = a.max_splits > 1 ? (int64_t)a.n_units * a.max_splits : 0;
-  carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc);
+  carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc, offset);
   return kca::launch_rows(q_dtype, kv_dtype, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
 }
 
@@ -497,6 +499,72 @@ int launch_multirow_route(const void* q, int32_t q_dtype, const void* k_cache, c
   const cudaError_t e = tc ? kca::launch_rows_tc(q_dtype, kv_dtype, tmk, tmv, a, s)
                            : kca::launch_decode_multirow(q_dtype, kv_dtype, tmk, tmv, a, s);
   return e == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+}
+
+// Plan of attn_decode_prefix: how the prefix is computed (route), the sequences'
+// own keys, and where everything lies in the workspace.
+//   kTc       q and cache of one 16-bit type, 3 or more sequences: the
+//             tensor-core prefill kernel, 16 sequences a row tile
+//   kUnits    another 16-bit cache, 2 or more sequences: multi-row units
+//   kRows     one sequence or an f32 cache: the decode kernels, each sequence
+//             over the whole prefix
+//   kNone     no query sees any of it
+struct PrefixPlan {
+  enum Route { kNone, kTc, kUnits, kRows } route;
+  int64_t kv_lo;               // first prefix position that a query may see
+  kca::TcPlan tc;
+  kca::RowsPlan pre, own;      // kUnits / kRows; the sequences' own keys
+  int pre_cluster, own_cluster;
+  int32_t unit_rows;
+  size_t own_rec, pre_rec, pre_parts, own_parts, total;   // byte offsets; bytes
+};
+
+// ctx: context lengths, or (dev) their bounds; KCA_OK or KCA_ERR_CUDA.
+int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t batch, const int64_t* ctx, bool dev,
+                int32_t window, PrefixPlan* out) {
+  PrefixPlan p{};
+  int sms = 0;
+  if (current_sms(&sms) != KCA_OK) return KCA_ERR_CUDA;
+  p.kv_lo = window > 0 ? prefix_len : 0;
+  for (int32_t b = 0; window > 0 && b < batch; ++b) {
+    // a device length may be as short as the prefix
+    const int64_t lo = kca::lo_of((dev ? prefix_len : ctx[b]) - 1, window);
+    if (lo < p.kv_lo) p.kv_lo = lo;
+  }
+  const bool same16 = q_dtype == kv_dtype && kv_dtype != KCA_F32;
+  p.route = p.kv_lo >= prefix_len                  ? PrefixPlan::kNone
+            : same16 && batch >= 3                 ? PrefixPlan::kTc
+            : kv_dtype != KCA_F32 && batch >= 2    ? PrefixPlan::kUnits
+                                                   : PrefixPlan::kRows;
+  const size_t rec = align_up(sizeof(float) * KCA_PARTIAL_FLOATS((size_t)batch));
+  p.own_rec = KCA_WORKSPACE_HEADER;
+  p.pre_rec = p.own_rec + rec;
+  p.pre_parts = p.pre_rec + (p.route == PrefixPlan::kRows ? rec : 0);
+  size_t need = KCA_WORKSPACE_HEADER;   // of the prefix's partials, a header included
+  int64_t nk[KCA_MAX_BATCH], lo = 0;
+  if (p.route == PrefixPlan::kTc) {
+    p.tc = kca::make_tc_prefix_plan(p.kv_lo, prefix_len, batch, window, sms / 2);
+    need = tc_ws_bytes(p.tc);
+  } else if (p.route == PrefixPlan::kUnits) {
+    p.unit_rows = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
+    const int32_t units = (batch + p.unit_rows - 1) / p.unit_rows;
+    for (int32_t u = 0; u < units; ++u) nk[u] = prefix_len - p.kv_lo;
+    p.pre = kca::make_rows_plan(units, nk, sms, kca::kMultiRowMinSplit);
+    const size_t slots = (size_t)batch * p.pre.max_splits;
+    need += align_up(slots * kHeads * 2 * 4) + align_up(slots * kHeads * kDim * 4);
+  } else if (p.route == PrefixPlan::kRows) {
+    for (int32_t b = 0; b < batch; ++b)
+      nk[b] = dev ? prefix_len - p.kv_lo : kca::shard_visible(ctx[b] - 1, window, 0, prefix_len, &lo);
+    p.pre = rows_plan(kv_dtype, batch, nk, sms, &p.pre_cluster, &need);
+    if (p.pre_cluster < 1) return KCA_ERR_CUDA;
+  }
+  p.own_parts = p.pre_parts + align_up(need - KCA_WORKSPACE_HEADER);
+  for (int32_t b = 0; b < batch; ++b) nk[b] = kca::shard_visible(ctx[b] - 1, window, prefix_len, 0, &lo);
+  p.own = rows_plan(kv_dtype, batch, nk, sms, &p.own_cluster, &need);
+  if (p.own_cluster < 1) return KCA_ERR_CUDA;
+  p.total = p.own_parts + align_up(need - KCA_WORKSPACE_HEADER);
+  *out = p;
+  return KCA_OK;
 }
 
 }  // namespace
@@ -1132,6 +1200,164 @@ int attn_decode_blocks(const void* q, int32_t q_dtype, const void* k_cache, cons
       !encode_kv_map(&tmv, v_cache, kv_dtype, 0, a.cache_rows, 64))
     return KCA_ERR_CUDA;
   return kca::launch_decode_mma_blocks(q_dtype, kv_dtype, tmk, tmv, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+}
+
+size_t attn_decode_prefix_workspace_bytes(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t batch,
+                                          const int64_t* ctx_len, int32_t window) {
+  if (ctx_len == nullptr || !dtype_ok(q_dtype) || !dtype_ok(kv_dtype) || batch < 1 || batch > KCA_MAX_BATCH ||
+      prefix_len < 0 || prefix_len > KCA_MAX_POSITION)
+    return 0;
+  for (int32_t b = 0; b < batch; ++b)
+    if (ctx_len[b] < prefix_len || ctx_len[b] > KCA_MAX_POSITION) return 0;
+  // enough for the lengths themselves and for device lengths up to them
+  PrefixPlan a, b;
+  if (plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx_len, false, window, &a) != KCA_OK ||
+      plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx_len, true, window, &b) != KCA_OK)
+    return 0;
+  return a.total > b.total ? a.total : b.total;
+}
+
+int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, const void* prefix_v, int64_t prefix_len,
+                       const void* k_cache, const void* v_cache, int32_t kv_dtype, int32_t n_q_heads,
+                       int32_t n_kv_heads, int32_t head_dim, int64_t capacity, int32_t batch, const int64_t* ctx_len,
+                       const int64_t* ctx_len_dev, int64_t ctx_bound, int32_t window, float scale, void* out,
+                       int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !out || !workspace || (ctx_len == nullptr && ctx_len_dev == nullptr))
+    return KCA_ERR_NULL;
+  if (prefix_len > 0 && (!prefix_k || !prefix_v)) return KCA_ERR_NULL;
+  int st = geometry_status(n_q_heads, n_kv_heads, head_dim);
+  if (st != KCA_OK) return st;
+  if (!dtype_ok(q_dtype) || !dtype_ok(kv_dtype) || (out_dtype != KCA_F32 && out_dtype != q_dtype)) return KCA_ERR_DTYPE;
+  if (ctx_len != nullptr && ctx_len_dev != nullptr) return KCA_ERR_RANGE;
+  if (prefix_len < 0 || prefix_len > KCA_MAX_POSITION || capacity < 1 || capacity > KCA_MAX_POSITION || batch < 1 ||
+      batch > KCA_MAX_BATCH || !std::isfinite(scale) || !(scale > 0.f))
+    return KCA_ERR_RANGE;
+  const int64_t most = prefix_len + capacity < KCA_MAX_POSITION ? prefix_len + capacity : KCA_MAX_POSITION;
+  int64_t ctx[KCA_MAX_BATCH];
+  for (int32_t b = 0; b < batch; ++b) {
+    ctx[b] = ctx_len != nullptr ? ctx_len[b] : ctx_bound;
+    if (ctx[b] < prefix_len || ctx[b] > most) return KCA_ERR_RANGE;
+  }
+  if (!aligned16(q) || !aligned16(prefix_k) || !aligned16(prefix_v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(out) || (reinterpret_cast<uintptr_t>(ctx_len_dev) % 8) != 0)
+    return KCA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0) return KCA_ERR_WORKSPACE;
+  PrefixPlan p;
+  st = plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx, ctx_len_dev != nullptr, window, &p);
+  if (st != KCA_OK) return st;
+  if (workspace_bytes < p.total) return KCA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  float* own_rec = reinterpret_cast<float*>(ws + p.own_rec);
+  kca::PrefixMergeArgs m{};
+  m.own = own_rec;
+  m.out = out;
+  m.ctx_dev = ctx_len_dev;
+  m.status = reinterpret_cast<kca::DeviceStatus*>(ws);
+  m.ctx_min = prefix_len;
+  m.ctx_bound = ctx_bound;
+  m.group = 1;
+  m.batch = batch;
+  m.out_dtype = out_dtype;
+  m.mscale = 1.4426950408889634f;
+
+  kca::RowsArgs r{};   // the rows kernels' arguments, common to prefix and own keys
+  r.q = q;
+  r.status = workspace;
+  r.n_units = batch;
+  r.window = window;
+  r.scale = scale;
+  r.ctx_dev = ctx_len_dev;
+  r.ctx_bound = ctx_bound;
+  for (int32_t b = 0; b < batch; ++b) r.ctx[b] = ctx[b];
+
+  if (p.route == PrefixPlan::kTc) {
+    kca::TcPrefixArgs a{};
+    a.plan = p.tc;
+    a.q = q;
+    a.status = workspace;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.ctx_dev = ctx_len_dev;
+    for (int32_t b = 0; b < batch; ++b) a.first_key[b] = (int32_t)kca::lo_of(ctx[b] - 1, window);
+    carve(workspace, (size_t)p.tc.n_slots * 128 * 2 * 4, &a.part_ml, &a.part_acc, p.pre_parts);
+    if (!kca::fill_tc_prefix_tables(a)) return KCA_ERR_RANGE;
+    CUtensorMap tmk, tmv, tmq, tmpart, tmpart_rag;
+    if (!encode_kv_map(&tmk, prefix_k, kv_dtype, p.kv_lo, prefix_len, 64) ||
+        !encode_kv_map(&tmv, prefix_v, kv_dtype, p.kv_lo, prefix_len, 64) ||
+        !encode_rows_map(&tmq, q, q_dtype, (int64_t)batch * kHeads, 64) ||
+        !encode_rows_map(&tmpart, a.part_acc, KCA_F32, (int64_t)p.tc.n_slots * 128, 32))
+      return KCA_ERR_CUDA;
+    const int32_t rag = batch % kca::kRowTile;   // the last tile stores its valid rows only
+    a.rag_tile = rag != 0 ? p.tc.n_tiles - 1 : -1;
+    tmpart_rag = tmpart;
+    if (rag != 0 && !encode_rows_map(&tmpart_rag, a.part_acc, KCA_F32, (int64_t)p.tc.n_slots * 128, 32,
+                                     (uint32_t)(rag * kHeads)))
+      return KCA_ERR_CUDA;
+    if (kca::launch_prefix_tc(kv_dtype, tmk, tmv, tmq, tmpart, tmpart_rag, a, s) != cudaSuccess) return KCA_ERR_CUDA;
+    m.ml = a.part_ml;
+    m.acc = a.part_acc;
+    m.group = kca::kRowTile;
+    m.group_step = (int64_t)p.tc.max_split * 128;
+    m.item_step = 128;
+    m.n_items = p.tc.max_split;
+    m.mscale = 1.f;
+  } else if (p.route == PrefixPlan::kUnits) {
+    kca::RowsArgs a = r;
+    a.k = prefix_k;
+    a.v = prefix_v;
+    a.mode = 3;
+    a.rows_per_seq = batch;
+    a.unit_rows = p.unit_rows;
+    a.n_units = p.pre.n_units;
+    a.split_len = p.pre.split_len;
+    a.max_splits = p.pre.max_splits;
+    a.key_begin = p.kv_lo;
+    a.key_end = prefix_len;
+    a.cache_rows = prefix_len;
+    a.part_slots = (int64_t)batch * a.max_splits;
+    carve(workspace, (size_t)a.part_slots * kHeads * 2 * 4, &a.part_ml, &a.part_acc, p.pre_parts);
+    CUtensorMap tmk, tmv;
+    if (!encode_kv_map(&tmk, prefix_k, kv_dtype, 0, prefix_len, 64) ||
+        !encode_kv_map(&tmv, prefix_v, kv_dtype, 0, prefix_len, 64) ||
+        kca::launch_rows_tc(q_dtype, kv_dtype, tmk, tmv, a, s) != cudaSuccess)
+      return KCA_ERR_CUDA;
+    m.ml = a.part_ml;
+    m.acc = a.part_acc;
+    m.group_step = (int64_t)a.max_splits * kHeads;
+    m.item_step = kHeads;
+    m.n_items = a.max_splits;
+  } else if (p.route == PrefixPlan::kRows) {
+    kca::RowsArgs a = r;
+    float* rec = reinterpret_cast<float*>(ws + p.pre_rec);
+    a.k = prefix_k;
+    a.v = prefix_v;
+    a.out_ml = rec;
+    a.out = rec + (size_t)batch * kHeads * 2;
+    a.seq_rows = 0;   // every sequence reads the same rows
+    a.key_end = prefix_len;
+    a.split_len = p.pre.split_len;
+    a.max_splits = p.pre.max_splits;
+    st = launch_rows_path(q_dtype, kv_dtype, prefix_k, prefix_v, prefix_len, a, p.pre_cluster, workspace, s,
+                          p.pre_parts);
+    if (st != KCA_OK) return st;
+    m.ml = a.out_ml;
+    m.acc = a.out;
+    m.group_step = kHeads;
+    m.n_items = 1;
+  }
+  r.k = k_cache;
+  r.v = v_cache;
+  r.out_ml = own_rec;
+  r.out = own_rec + (size_t)batch * kHeads * 2;
+  r.seq_rows = capacity;
+  r.key_begin = prefix_len;
+  r.key_end = prefix_len + capacity;
+  r.split_len = p.own.split_len;
+  r.max_splits = p.own.max_splits;
+  st = launch_rows_path(q_dtype, kv_dtype, k_cache, v_cache, (int64_t)batch * capacity, r, p.own_cluster, workspace, s,
+                        p.own_parts);
+  if (st != KCA_OK) return st;
+  return kca::launch_prefix_merge(m, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
 }
 
 int attn_merge_partials(int32_t n_parts, int32_t batch, const float* parts, int64_t part_stride, float* out,

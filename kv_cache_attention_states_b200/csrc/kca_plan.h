@@ -237,6 +237,31 @@ KCA_HD TcItem tc_item(const TcPlan& p, int32_t idx) {
   return it;
 }
 
+// Plan of the rows of a batch over a prefix that all of them share: every row
+// tile sees the keys [kv_lo, prefix_len) (a row masks what its window cuts
+// off), every pair gets the same number of items, and every item writes a
+// partial.  Slot of (tile t, item k): t * max_split + k.
+inline TcPlan make_tc_prefix_plan(int64_t kv_lo, int64_t prefix_len, int32_t rows, int32_t window,
+                                  int32_t pair_budget) {
+  TcPlan p{};
+  p.rows = rows;
+  p.window = window;
+  p.kv_lo = kv_lo;
+  p.ctx_len = prefix_len;
+  p.n_tiles = (int32_t)cdiv(rows, kRowTile);
+  p.n_pairs = (int32_t)cdiv(p.n_tiles, 2);
+  const int32_t n = (int32_t)cdiv(prefix_len - kv_lo, kKeyTile);
+  const int32_t budget = pair_budget > 80 ? 80 : pair_budget;   // the launch's item table
+  int32_t s = budget / p.n_pairs;
+  if (s < 1) s = 1;
+  p.per_item = (int32_t)cdiv(n, s);
+  if (p.per_item < kTcMinItemTiles) p.per_item = kTcMinItemTiles;
+  p.max_split = (int32_t)cdiv(n, p.per_item);
+  p.n_items = p.n_pairs * p.max_split;
+  p.n_slots = p.n_tiles * p.max_split;
+  return p;
+}
+
 // pair_budget: CTA pairs that run at once (one wave).
 inline TcPlan make_tc_plan(int64_t chunk_start, int32_t rows, int32_t window, int32_t pair_budget) {
   TcPlan p{};

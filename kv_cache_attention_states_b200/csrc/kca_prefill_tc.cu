@@ -48,6 +48,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kca_common.cuh"
 #include "kca_plan.h"
 #include "kca_tc.h"
@@ -181,12 +183,15 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int DT>
+// Args: TcArgs (a chunk's causal rows) or TcPrefixArgs (a batch's queries over
+// their shared prefix, which differ in their rows' masks only).
+template <int DT, class Args>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmo,
                       const __grid_constant__ CUtensorMap tmpart,
-                      const __grid_constant__ CUtensorMap tmpart_rag, const TcArgs a) {
+                      const __grid_constant__ CUtensorMap tmpart_rag, const Args a) {
+  constexpr bool kPrefix = std::is_same<Args, TcPrefixArgs>::value;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = ((raw_addr + 1023u) & ~1023u) - raw_addr;
@@ -362,8 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int64_t row = (int64_t)tile * kRowTile + (m >> 3);
     const bool valid = row < a.plan.rows;
-    const int64_t pos = a.plan.chunk_start + row;
-    const int64_t lo = lo_of(pos, a.plan.window);
+    int64_t pos = a.plan.chunk_start + row;
+    int64_t lo = lo_of(pos, a.plan.window);
+    if constexpr (kPrefix) {
+      pos = a.plan.ctx_len - 1;   // the whole prefix lies before every query
+      lo = !valid || a.plan.window <= 0 ? 0
+           : a.ctx_dev != nullptr       ? lo_of(a.ctx_dev[row] - 1, a.plan.window)
+                                        : a.first_key[row];
+    }
 
     const float cs = a.scale_log2;
     const uint32_t scol = kColS + 64 * wg;
@@ -628,15 +639,15 @@ __global__ void __launch_bounds__(256) merge_tc_kernel(const TcArgs a) {
   dst[1] = make_float4(A1.x * inv, A1.y * inv, A1.z * inv, A1.w * inv);
 }
 
-template <int DT>
+template <int DT, class Args>
 cudaError_t launch_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq,
                      const CUtensorMap& tmo, const CUtensorMap& tmpart, const CUtensorMap& tmpart_rag,
-                     const TcArgs& a, cudaStream_t stream) {
+                     const Args& a, cudaStream_t stream) {
   static std::atomic<bool> attr_set[64];   // per device; zero-initialised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<DT>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<DT, Args>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -657,8 +668,8 @@ cudaError_t launch_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const CUten
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<DT>, tmk, tmv, tmq, tmo, tmpart, tmpart_rag, a);
-  if (e != cudaSuccess || a.plan.n_slots == 0) return e;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<DT, Args>, tmk, tmv, tmq, tmo, tmpart, tmpart_rag, a);
+  if (std::is_same<Args, TcPrefixArgs>::value || e != cudaSuccess || a.plan.n_slots == 0) return e;
   int ns_max = 0;
   for (int32_t t = 0; t < a.plan.n_tiles && t < kTcMaxTiles; ++t)
     ns_max = a.tile_items[t] > ns_max ? a.tile_items[t] : ns_max;
@@ -725,6 +736,31 @@ cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tmk, const CUtensorM
                               const TcArgs& a, cudaStream_t stream) {
   if (dtype == KCA_BF16) return launch_t<KCA_BF16>(tmk, tmv, tmq, tmo, tmpart, tmpart_rag, a, stream);
   if (dtype == KCA_F16) return launch_t<KCA_F16>(tmk, tmv, tmq, tmo, tmpart, tmpart_rag, a, stream);
+  return cudaErrorInvalidValue;
+}
+
+bool fill_tc_prefix_tables(TcPrefixArgs& a) {
+  const int32_t s = a.plan.max_split;
+  const int32_t n = (int32_t)cdiv(a.plan.ctx_len - a.plan.kv_lo, (int64_t)kKeyTile);
+  if (s < 1 || s > n || a.plan.n_tiles < 1 || a.plan.n_tiles > kTcMaxTiles || a.plan.n_items > kTcMaxItems ||
+      a.plan.n_items != a.plan.n_pairs * s || a.plan.n_slots != a.plan.n_tiles * s)
+    return false;
+  for (int32_t i = 0; i < a.plan.n_items && i < kTcMaxItems; ++i) {
+    const int32_t q = i / s, k = i % s;
+    a.items[i].kt_begin = tc_split_at(n, s, k);
+    a.items[i].kt_end = tc_split_at(n, s, k + 1);
+    a.items[i].pair = (int16_t)q;
+    a.items[i].slot[0] = (int16_t)(2 * q * s + k);
+    a.items[i].slot[1] = (int16_t)(2 * q + 1 < a.plan.n_tiles ? (2 * q + 1) * s + k : -1);
+  }
+  return true;
+}
+
+cudaError_t launch_prefix_tc(int dtype, const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq,
+                             const CUtensorMap& tmpart, const CUtensorMap& tmpart_rag, const TcPrefixArgs& a,
+                             cudaStream_t stream) {
+  if (dtype == KCA_BF16) return launch_t<KCA_BF16>(tmk, tmv, tmq, tmpart, tmpart, tmpart_rag, a, stream);
+  if (dtype == KCA_F16) return launch_t<KCA_F16>(tmk, tmv, tmq, tmpart, tmpart, tmpart_rag, a, stream);
   return cudaErrorInvalidValue;
 }
 

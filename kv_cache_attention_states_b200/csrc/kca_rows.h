@@ -8,6 +8,8 @@
 
 namespace kca {
 
+struct DeviceStatus;
+
 struct RowsArgs {
   const void* q;         // [n_units][8][256]
   const void* k;         // cache rows
@@ -19,7 +21,10 @@ struct RowsArgs {
   int64_t seq_rows;      // decode, batched rows: cache rows per sequence (capacity)
   int64_t chunk_start;   // prefill: position of unit 0
   int32_t mode;          // 0: decode (unit = sequence), 1: prefill (unit = row of sequence 0),
-                         // 2: batched rows (unit = row i of sequence unit / rows_per_seq)
+                         // 2: batched rows (unit = row i of sequence unit / rows_per_seq),
+                         // 3: launch_rows_tc only: multi-row units of a batch's queries over
+                         //    the keys [key_begin, key_end) that the batch shares; every split
+                         //    writes its partial, nothing merges them
   int32_t rows_per_seq;  // mode 2: query rows per sequence, at ctx[b] - rows_per_seq .. ctx[b] - 1
   int32_t unit_rows;     // multi-row units: rows per unit (kMultiRows, or kMultiRowsWide for tcgen05)
   int32_t n_units;
@@ -219,6 +224,24 @@ cudaError_t launch_rows_tc(int q_dtype, int kv_dtype, const CUtensorMap& tmk, co
 // set); with more, a.tickets is null and launch_rows_tc adds the merge kernel.
 constexpr int kRowsTcMergeSplits = 16;
 cudaError_t launch_multirow_merge(const RowsArgs& a, cudaStream_t stream);
+
+// Merge of attn_decode_prefix (kca_prefix.cu): row (b, h) of the output is the
+// log-sum-exp combination of n_items partials of the prefix -- item s at index
+// (b / group) * group_step + s * item_step + (b % group) * 8 + h of ml / acc --
+// and the record of the sequence's own keys (layout of attn_decode_partial).
+struct PrefixMergeArgs {
+  const float* ml;
+  const float* acc;
+  const float* own;
+  void* out;
+  const int64_t* ctx_dev;   // lengths outside ctx_min..ctx_bound: zeros, recorded
+  DeviceStatus* status;
+  int64_t ctx_min, ctx_bound;
+  int64_t group_step, item_step;
+  int32_t group, n_items, batch, out_dtype;
+  float mscale;             // the items' m to log2 units
+};
+cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, cudaStream_t stream);
 
 // Clusters of c CTAs of the tensor-core rows kernel that fit on the device at
 // once (0 on failure).

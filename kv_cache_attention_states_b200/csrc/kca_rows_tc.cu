@@ -160,9 +160,11 @@ __global__ void __launch_bounds__(RowsTc<UR>::kThreads, 1)
   const int lane = threadIdx.x & 31;
   int b, i0, nr;
   multirow_unit(a, unit, &b, &i0, &nr);
+  // mode 3: the rows are a batch's queries, all past the shared keys
+  const bool shared = a.mode == 3;
   const int64_t pos0 = a.ctx[b] - a.rows_per_seq + i0;   // first row's position
-  const int64_t lo_u = lo_of(pos0, a.window);
-  const int64_t hi_u = pos0 + nr - 1;
+  const int64_t lo_u = shared ? a.key_begin : lo_of(pos0, a.window);
+  const int64_t hi_u = shared ? a.key_end - 1 : pos0 + nr - 1;
   const int32_t nsplit = rows_n_splits(hi_u - lo_u + 1, a.split_len);
   if (split >= nsplit) return;
   const int64_t kbeg = lo_u + (int64_t)split * a.split_len;
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(RowsTc<UR>::kThreads, 1)
   // bounds-checked builds: the split's rows in the cache, its rows' partial
   // slots in the workspace (no CTA of this kernel waits on another)
   if (!KCA_IN_BOUNDS(nsplit <= a.max_splits && base_row + kbeg >= 0 && base_row + kend <= a.cache_rows &&
-                         (nsplit == 1 || (((int64_t)b * a.rows_per_seq + i0 + nr) * a.max_splits <= a.part_slots &&
-                                          unit < kRTickets)),
+                         ((nsplit == 1 && !shared) || (((int64_t)b * a.rows_per_seq + i0 + nr) * a.max_splits <= a.part_slots &&
+                                               (shared || unit < kRTickets))),
                      status, kSiteBoundsMulti, (unsigned)unit))
     return;
 
@@ -351,8 +353,8 @@ __global__ void __launch_bounds__(RowsTc<UR>::kThreads, 1)
     const int i = 2 * q + ((lane >> 3) & 1), h = lane & 7;
     const bool valid = i < nr;
     const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
-    const int64_t pos = pos0 + i;
-    const int64_t lo = lo_of(pos, a.window);
+    const int64_t pos = shared ? hi_u : pos0 + i;
+    const int64_t lo = shared ? (valid ? lo_of(rows_ctx(a, i0 + i, false) - 1, a.window) : 0) : lo_of(pos, a.window);
     const float cs = a.scale * 1.4426950408889634f;  // scores in log2 units
     const int cofs = 16 * g + (low ? 8 : 0);         // this lane's 8 columns within a stage
     float m_ref = -INFINITY;                         // reference max of the row, log2 units
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(RowsTc<UR>::kThreads, 1)
     float* dst = nullptr;
     float f = 1.f;
     if (valid) {
-      if (nsplit == 1) {
+      if (nsplit == 1 && !shared) {
         dst = a.out + (orow * kHeads + h) * kDim + 64 * g + (low ? 32 : 0);
         f = (m_ref == -INFINITY && L == 0.f) ? 0.f : 1.f / L;
       } else {
@@ -587,7 +589,7 @@ cudaError_t launch_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const RowsA
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a);
-  if (e != cudaSuccess || a.max_splits <= 1 || a.tickets != nullptr) return e;
+  if (e != cudaSuccess || a.mode == 3 || a.max_splits <= 1 || a.tickets != nullptr) return e;
   return launch_multirow_merge(a, stream);
 }
 

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/kca.h"
 #include "kca_plan.h"
 
 namespace kca {
@@ -33,6 +34,19 @@ struct TcArgs {
   int16_t tile_first_slot[kTcMaxTiles];
   int16_t tile_items[kTcMaxTiles];
 };
+
+// Decode of a batch over a shared prefix (attn_decode_prefix): the rows are the
+// batch's queries, each seeing the prefix from its window's first key on.
+struct TcPrefixArgs : TcArgs {
+  const int64_t* ctx_dev;        // context lengths, or null: first_key
+  int32_t first_key[KCA_MAX_BATCH];
+};
+// Fills the item table of a make_tc_prefix_plan; false when it would not fit.
+bool fill_tc_prefix_tables(TcPrefixArgs& a);
+// As launch_prefill_tc, without the merge: the partials are the result.
+cudaError_t launch_prefix_tc(int dtype, const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq,
+                             const CUtensorMap& tmpart, const CUtensorMap& tmpart_rag, const TcPrefixArgs& a,
+                             cudaStream_t stream);
 
 // Fills the item and tile tables from a.plan; false when they would not fit
 // the plan (launch tables, partial slots or the keys the maps cover).

@@ -29,3 +29,13 @@ def rounded(want, bound, out_dtype):
     """bound plus the rounding of the output to its type (half a step; f16
     subnormals 2^-25)."""
     return bound + HALF_STEP[out_dtype] * (np.abs(want) + bound) + (2.0 ** -25 if out_dtype == "f16" else 1e-38)
+
+
+def rounded_probabilities(kv_dtype, absqk, vmax, pabsv, n_keys):
+    """Bound of kernels that round each probability to the cache's type once
+    (q of that type): the f32 part as in f32_grade without its probabilities'
+    parts, half a step of sum p |v| / sum p, and for f16 the subnormal
+    probabilities (2^-25 each against a sum of at least 1)."""
+    f32 = (2 * np.asarray(absqk)[:, None] * 2.0 ** -18 + 2.0 ** -17) * vmax
+    sub = n_keys * 2.0 ** -25 * vmax if kv_dtype == "f16" else 0.0
+    return f32 + HALF_STEP[kv_dtype] * pabsv + sub

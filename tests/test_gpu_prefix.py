@@ -1,0 +1,266 @@
+"""GPU parity of attn_decode_prefix (decode of a batch over a prefix that it
+shares) against the f64 oracle: every route (tensor-core tiles, multi-row units,
+decode kernels), windows that cut the prefix, single keys on both sides of every
+border, device lengths, captured steps, streams."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_attention_states_b200 as kca
+from kv_cache_attention_states_b200 import synth
+from oracle import prefix as op
+from tests.helpers import dev
+from tests.helpers_bounds import f32_grade, rounded, rounded_probabilities
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup(cuda_ok):
+    kca.lib()
+
+
+def _i64(x):
+    return torch.tensor(np.asarray(x, dtype=np.int64), device="cuda")
+
+
+def _data(seed, batch, prefix, cap, qd, kv):
+    return (synth.draw(seed, "q", (batch, 8, 256), qd), synth.draw(seed, "pk", (prefix, 256), kv),
+            synth.draw(seed, "pv", (prefix, 256), kv), synth.draw(seed, "k", (batch, cap, 256), kv),
+            synth.draw(seed, "v", (batch, cap, 256), kv))
+
+
+def _check(got, od, data, qd, kv, ctx, window, seqs=None):
+    q, pk, pv, k, v = data
+    got = got.float().cpu().numpy().astype(np.float64)
+    tc = qd == kv and kv != "f32" and len(ctx) >= 3
+    for b in seqs if seqs is not None else range(len(ctx)):
+        want, absqk, vmax, pabsv, n = op.attend(q[b], qd, pk, pv, k[b], v[b], kv, ctx[b], window)
+        base = rounded_probabilities(kv, absqk, vmax, pabsv, n) if tc else f32_grade(qd, kv, absqk, vmax)[:, None]
+        worst = float(np.max(np.abs(got[b] - want) / rounded(want, base, od)))
+        assert worst <= 1.0, (b, worst)
+
+
+def _run(data, qd, kv, ctx, window=0, od="f32", device=False, ws=None, out=None, bound=None, stream=None, prefix=None):
+    q, pk, pv, k, v = data
+    prefix = pk.shape[0] if prefix is None else prefix
+    if out is None:
+        out = torch.full((len(ctx), 8, 256), 5.0, dtype=synth.torch_dtype(od), device="cuda")
+    got = kca.attn_decode_prefix(dev(q, qd), dev(pk, kv), dev(pv, kv), prefix, dev(k, kv), dev(v, kv),
+                                 _i64(ctx) if device else ctx, window=window, ctx_bound=bound, out=out, workspace=ws,
+                                 stream=stream)
+    assert got is out
+    return got
+
+
+PAIRS = [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("f32", "f16", "f32"), ("f32", "bf16", "f32"),
+         ("f32", "f32", "f32"), ("f16", "bf16", "f16"), ("bf16", "f32", "bf16")]
+
+
+@pytest.mark.parametrize("qd,kv,od", PAIRS)
+@pytest.mark.parametrize("batch,prefix,cap", [(1, 300, 70), (2, 1, 64), (3, 1000, 77), (5, 129, 1), (9, 2600, 300),
+                                              (17, 700, 33), (33, 260, 20)])
+@pytest.mark.parametrize("device", [False, True])
+def test_matches_oracle(qd, kv, od, batch, prefix, cap, device):
+    data = _data(40, batch, prefix, cap, qd, kv)
+    ctx = [prefix + int(c) for c in synth.integers(41, "c", 0, cap, batch)]
+    ctx[0], ctx[-1] = prefix + cap, prefix
+    _check(_run(data, qd, kv, ctx, od=od, device=device), od, data, qd, kv, ctx, 0)
+
+
+@pytest.mark.parametrize("qd,kv,od", PAIRS)
+@pytest.mark.parametrize("batch,prefix,cap,window", [(4, 900, 400, 300), (20, 900, 40, 333), (3, 128, 200, 1),
+                                                     (2, 500, 100, 64), (1, 1000, 30, 500), (40, 700, 90, 5000)])
+@pytest.mark.parametrize("device", [False, True])
+def test_windows_cut_the_prefix(qd, kv, od, batch, prefix, cap, window, device):
+    data = _data(42, batch, prefix, cap, qd, kv)
+    ctx = [prefix + int(c) for c in synth.integers(43, "c", 0, cap, batch)]
+    ctx[0] = prefix + cap
+    _check(_run(data, qd, kv, ctx, window, od, device), od, data, qd, kv, ctx, window)
+
+
+@pytest.mark.parametrize("qd,kv", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("device", [False, True])
+def test_border_keys(qd, kv, window, device):
+    """One key of each sequence draws nearly all of its weight when it is seen;
+    the keys chosen lie on each side of every border."""
+    prefix, cap = 385, 70
+    ctx = [prefix + c for c in (0, 1, 2, 64, 65, 70, 33)]
+    data = _data(44, len(ctx), prefix, cap, qd, kv)
+    q, pk, pv, k, v = data
+    for b in range(len(ctx)):
+        first = max(0, ctx[b] - window) if window else 0
+        for p in (first, first - 1, prefix - 1, prefix, ctx[b] - 1, ctx[b], 127, 128, 0):
+            if not 0 <= p < prefix + cap:
+                continue
+            q1, k1, v1 = q.copy(), k.copy(), v.copy()
+            pk1, pv1 = pk.copy(), pv.copy()
+            one, three = (np.uint16(0x3F80), np.uint16(0x4040)) if kv == "bf16" else (1.0, 3.0)
+            qone = np.uint16(0x3F80) if qd == "bf16" else 1.0
+            q1[b] = qone
+            (pk1 if p < prefix else k1[b])[p if p < prefix else p - prefix] = one     # score 16 against N(0, 1)
+            (pv1 if p < prefix else v1[b])[p if p < prefix else p - prefix] = three
+            d = (q1, pk1, pv1, k1, v1)
+            got = _run(d, qd, kv, ctx, window, device=device)
+            _check(got, "f32", d, qd, kv, ctx, window, seqs=[b])
+            assert bool((got[b] > 2.5).all()) == (first <= p < ctx[b]), (b, p)
+
+
+@pytest.mark.parametrize("qd,kv", [("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
+def test_no_key_and_no_prefix(qd, kv):
+    data = _data(45, 4, 300, 90, qd, kv)
+    for device in (False, True):
+        ctx = [90, 1, 0, 33]                                     # prefix_len 0: plain decode
+        got = _run(data, qd, kv, ctx, device=device, prefix=0, bound=90)
+        empty = (data[0], data[1][:0], data[2][:0], data[3], data[4])
+        _check(got, "f32", empty, qd, kv, ctx, 0)
+        assert bool((got[2] == 0).all())
+    q, pk, pv, k, v = data
+    got = kca.attn_decode_prefix(dev(q, qd), None, None, 0, dev(k, kv), dev(v, kv), [90, 1, 0, 33])
+    assert bool((got[2] == 0).all())
+    ctx = [390, 360, 381, 350]                                   # a window that no prefix key passes
+    _check(_run(data, qd, kv, ctx, 50), "f32", data, qd, kv, ctx, 50)
+
+
+@pytest.mark.parametrize("qd,kv", [("f16", "f16"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("window", [0, 150])
+def test_rows_that_no_query_sees_may_hold_anything(qd, kv, window):
+    prefix, cap, batch = 333, 50, 5
+    data = _data(46, batch, prefix, cap, qd, kv)
+    ctx = [prefix + c for c in (50, 0, 1, 30, 49)]
+    q, pk, pv, k, v = (torch.cat((dev(x, d), dev(x, d)[:1] * 0)) if i in (1, 2) else dev(x, d)
+                       for i, (x, d) in enumerate(zip(data, (qd, kv, kv, kv, kv))))
+    for b, c in enumerate(ctx):
+        k[b, c - prefix:], v[b, c - prefix:] = float("nan"), float("inf")
+    pk[prefix:], pv[prefix:] = float("nan"), float("nan")        # a longer buffer than the prefix
+    if window:
+        pk[:prefix - window], pv[:prefix - window] = float("inf"), float("nan")
+    got = kca.attn_decode_prefix(q, pk, pv, prefix, k, v, ctx, window)
+    _check(got, "f32", data, qd, kv, ctx, window)
+
+
+def test_bad_device_lengths_give_zeros_and_are_recorded():
+    prefix, cap, batch = 500, 60, 6
+    for qd, kv in (("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")):
+        data = _data(47, batch, prefix, cap, qd, kv)
+        ctx = [540, 499, 561, -1, 560, 1 << 40]
+        ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(
+            *[{"f32": kca.F32, "f16": kca.F16, "bf16": kca.BF16}[d] for d in (qd, kv)], prefix, [560] * batch, 100))
+        got = _run(data, qd, kv, ctx, 100, device=True, ws=ws)
+        _check(got, "f32", data, qd, kv, ctx, 100, seqs=[0, 4])
+        for b in (1, 2, 3, 5):
+            assert bool((got[b] == 0).all())
+        st, detail = kca.attn_device_status(ws)
+        assert st == -8 and detail >> 24 == 10 and detail & 0xFFFFFF in (1, 2, 3, 5)
+        assert kca.attn_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("qd,kv,batch,prefix", [("f16", "f16", 256, 5000), ("bf16", "bf16", 64, 20000),
+                                                ("f16", "f16", 3, 131000), ("f32", "f16", 50, 3000),
+                                                ("f32", "f16", 8, 40000), ("bf16", "bf16", 1, 100000)])
+def test_large(qd, kv, batch, prefix):
+    data = _data(48, batch, prefix, 72, qd, kv)
+    ctx = [prefix + int(c) for c in synth.integers(49, "c", 1, 72, batch)]
+    got = _run(data, qd, kv, ctx)
+    _check(got, "f32", data, qd, kv, ctx, 0, seqs=sorted({0, 1 % batch, batch // 2, batch - 1}))
+    again = _run(data, qd, kv, ctx)
+    assert torch.equal(got, again)                               # the same bits on every call
+
+
+def test_large_scores_in_one_sequence_only():
+    """Row maxima that rise along the prefix (every rescale), beside rows of
+    small scores in the same tile."""
+    prefix, cap, batch = 3000, 40, 6
+    data = _data(50, batch, prefix, cap, "f16", "f16")
+    q, pk, pv, k, v = data
+    ramp = np.linspace(0, 3, prefix).astype(np.float16)[:, None]
+    pk[:] = ramp * np.sign(q[2, 0].astype(np.float32)).astype(np.float16)[None]
+    ctx = [prefix + 7] * batch
+    _check(_run(data, "f16", "f16", ctx), "f32", data, "f16", "f16", ctx, 0)
+
+
+@pytest.mark.parametrize("qd,kv,batch", [("bf16", "bf16", 4), ("f32", "f16", 3), ("f32", "f32", 2)])
+@pytest.mark.parametrize("window", [0, 400])
+def test_captured_step_follows_device_lengths(qd, kv, batch, window):
+    """append + decode over the shared prefix, captured once on another stream
+    and replayed as the sequences grow."""
+    prefix, cap = 777, 130
+    data = _data(51, batch, prefix, cap, qd, kv)
+    q, pk, pv, k, v = data
+    qt, pkt, pvt, src_k, src_v = dev(q, qd), dev(pk, kv), dev(pv, kv), dev(k, kv), dev(v, kv)
+    kt, vt = torch.zeros_like(src_k), torch.zeros_like(src_v)
+    ctx = _i64([prefix] * batch)
+    nk, nv = torch.empty((batch, 256), device="cuda"), torch.empty((batch, 256), device="cuda")
+    dst = torch.zeros(batch, dtype=torch.int64, device="cuda")
+    out = torch.empty((batch, 8, 256), dtype=torch.float32, device="cuda")
+    ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(kca.dtype_code(qt), kca.dtype_code(kt), prefix,
+                                                                  [prefix + cap] * batch, window))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        kca.attn_append_kv(nk, nv, kt.view(-1, 256), vt.view(-1, 256), dst, workspace=ws, stream=stream)
+        kca.attn_decode_prefix(qt, pkt, pvt, prefix, kt, vt, ctx, window, out=out, workspace=ws, stream=stream)
+
+    step()                                                       # not captured: row 0 is written again below
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for t in range(3):
+        nk.copy_(src_k[:, t].float())
+        nv.copy_(src_v[:, t].float())
+        ctx.copy_(_i64([prefix + t + 1] * batch))
+        dst.copy_(_i64([b * cap + t for b in range(batch)]))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, "f32", data, qd, kv, [prefix + t + 1] * batch, window)
+    assert kca.attn_device_status(ws)[0] == 0
+
+
+def test_two_streams_at_once():
+    cases = [("bf16", "bf16", 5, 4000), ("f32", "f16", 4, 3000)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    sets = []
+    for i, (qd, kv, batch, prefix) in enumerate(cases):
+        data = _data(52 + i, batch, prefix, 90, qd, kv)
+        ctx = [prefix + int(c) for c in synth.integers(53, "c", 1, 90, batch)]
+        t = [dev(x, d) for x, d in zip(data, (qd, kv, kv, kv, kv))]
+        ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(kca.dtype_code(t[0]), kca.dtype_code(t[1]), prefix,
+                                                                      ctx))
+        sets.append((data, t, ctx, ws, []))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (data, t, ctx, ws, outs), (qd, kv, batch, prefix) in zip(streams, sets, cases):
+            with torch.cuda.stream(st):
+                outs.append(kca.attn_decode_prefix(t[0], t[1], t[2], prefix, t[3], t[4], ctx, workspace=ws, stream=st))
+    torch.cuda.synchronize()
+    for (data, t, ctx, ws, outs), (qd, kv, batch, prefix) in zip(sets, cases):
+        _check(outs[0], "f32", data, qd, kv, ctx, 0)
+        assert all(torch.equal(o, outs[0]) for o in outs)
+        assert kca.attn_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("qd,kv,batch", [("bf16", "bf16", 20), ("f32", "f16", 9), ("f32", "f32", 4), ("f16", "f16", 1)])
+@pytest.mark.parametrize("device", [False, True])
+def test_through_the_checked_build(qd, kv, batch, device):
+    """The bounds-checked build records nothing and gives the same bits."""
+    prefix, cap, window = 2500, 80, 1999
+    data = _data(55, batch, prefix, cap, qd, kv)
+    ctx = [prefix + int(c) for c in synth.integers(56, "c", 0, cap, batch)]
+    codes = {"f32": kca.F32, "f16": kca.F16, "bf16": kca.BF16}
+    ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(codes[qd], codes[kv], prefix, [prefix + cap] * batch,
+                                                                  window))
+    a = _run(data, qd, kv, ctx, window, device=device, ws=ws)
+    torch.cuda.synchronize()
+    saved = kca._lib
+    kca._lib = kca.load_library(kca.LIB_CHECKED_PATH)
+    try:
+        b = _run(data, qd, kv, ctx, window, device=device, ws=ws)
+        torch.cuda.synchronize()
+        assert kca.attn_device_status(ws)[0] == 0
+    finally:
+        kca._lib = saved
+    assert torch.equal(a, b)
