@@ -41,7 +41,9 @@ __device__ __forceinline__ uint32_t block_code(float x, float sx) {
 // ---------------------------------------------------------------- summaries
 // One CTA per finished block: warp w takes keys 8 w .. 8 w + 7, lane l dims
 // 8 l .. 8 l + 7 (eight 16-byte loads in flight per thread for 16-bit keys),
-// the warps' bounds meet in shared memory, and thread t quantises dim t.
+// the warps' bounds meet in shared memory, and the threads quantise them.
+// 16-bit keys stay packed until then: two values per maximum, and half the
+// exchange.
 // Bound: memory (32 KiB of 16-bit keys in, 516 bytes out).
 struct SummaryArgs {
   const void* k;
@@ -53,9 +55,28 @@ struct SummaryArgs {
   int32_t n_blocks;        // blocks per sequence of codes / scales
 };
 
+// Largest / smallest values of two packed 16-bit pairs, NaN where either is.
+template <int KT, bool MAX>
+__device__ __forceinline__ uint32_t pick2(uint32_t a, uint32_t b) {
+  if (KT == KCA_F16) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&b);
+    const __half2 z = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+    return *reinterpret_cast<const uint32_t*>(&z);
+  }
+  const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a), y = *reinterpret_cast<const __nv_bfloat162*>(&b);
+  const __nv_bfloat162 z = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+template <int KT, bool MAX>
+__device__ __forceinline__ uint4 pick8(uint4 a, uint4 b) {
+  return make_uint4(pick2<KT, MAX>(a.x, b.x), pick2<KT, MAX>(a.y, b.y), pick2<KT, MAX>(a.z, b.z),
+                    pick2<KT, MAX>(a.w, b.w));
+}
+
 template <int KT>
 __global__ void __launch_bounds__(256) summarize_kernel(const SummaryArgs a) {
-  __shared__ float hi_s[8][kDim], lo_s[8][kDim];
+  constexpr int kRow = kDim * ElemBytes<KT>::value;   // bytes of a key
+  __shared__ __align__(16) unsigned char ex[2][8][kRow];   // the warps' largest and smallest values
   __shared__ float am_s[8];
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -69,37 +90,64 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SummaryArgs a) {
   const int64_t old = ctx > a.n_new ? ctx - a.n_new : 0;
   const int64_t j = old / kBlockKeys + blockIdx.x;
   if (j >= ctx / kBlockKeys) return;
-  const char* rows = static_cast<const char*>(a.k) +
-                     (((int64_t)b * a.capacity + j * kBlockKeys + 8 * warp) * kDim + 8 * lane) * ElemBytes<KT>::value;
-  float x[8][8];
+  const char* rows = static_cast<const char*>(a.k) + ((int64_t)b * a.capacity + j * kBlockKeys + 8 * warp) * kRow;
+  const int t = threadIdx.x;
+  float v[2];   // 16-bit: dims 2 (t % 128) and + 1 of hi (t < 128) or lo; f32: hi and lo of dim t
+  if constexpr (KT == KCA_F32) {
+    float x[8][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load8<KT>(rows + (int64_t)i * kDim * ElemBytes<KT>::value, x[i]);
+    for (int i = 0; i < 8; ++i) load8<KT>(rows + i * kRow + 32 * lane, x[i]);
+    float* hd = reinterpret_cast<float*>(ex[0][warp]) + 8 * lane;
+    float* ld = reinterpret_cast<float*>(ex[1][warp]) + 8 * lane;
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    float h = x[0][t], l = x[0][t];
+    for (int c = 0; c < 8; ++c) {
+      float h = x[0][c], l = x[0][c];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        h = max_nan(h, x[i][c]);
+        l = min_nan(l, x[i][c]);
+      }
+      hd[c] = h;
+      ld[c] = l;
+    }
+    __syncthreads();
+    v[0] = reinterpret_cast<const float*>(ex[0][0])[t];
+    v[1] = reinterpret_cast<const float*>(ex[1][0])[t];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      v[0] = max_nan(v[0], reinterpret_cast<const float*>(ex[0][w])[t]);
+      v[1] = min_nan(v[1], reinterpret_cast<const float*>(ex[1][w])[t]);
+    }
+  } else {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(rows + i * kRow + 16 * lane);
+    uint4 h = x[0], l = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
-      h = max_nan(h, x[i][t]);
-      l = min_nan(l, x[i][t]);
+      h = pick8<KT, true>(h, x[i]);
+      l = pick8<KT, false>(l, x[i]);
     }
-    x[0][t] = h;
-    x[1][t] = l;
-  }
-  float4* hd = reinterpret_cast<float4*>(&hi_s[warp][8 * lane]);
-  float4* ld = reinterpret_cast<float4*>(&lo_s[warp][8 * lane]);
-  hd[0] = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
-  hd[1] = make_float4(x[0][4], x[0][5], x[0][6], x[0][7]);
-  ld[0] = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
-  ld[1] = make_float4(x[1][4], x[1][5], x[1][6], x[1][7]);
-  __syncthreads();
-  const int t = threadIdx.x;
-  float h = hi_s[0][t], l = lo_s[0][t];
+    *reinterpret_cast<uint4*>(ex[0][warp] + 16 * lane) = h;
+    *reinterpret_cast<uint4*>(ex[1][warp] + 16 * lane) = l;
+    __syncthreads();
+    const int p = t & 127;
+    uint32_t u;
+    if (t < 128) {
+      u = reinterpret_cast<const uint32_t*>(ex[0][0])[p];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) {
-    h = max_nan(h, hi_s[w][t]);
-    l = min_nan(l, lo_s[w][t]);
+      for (int w = 1; w < 8; ++w) u = pick2<KT, true>(u, reinterpret_cast<const uint32_t*>(ex[0][w])[p]);
+    } else {
+      u = reinterpret_cast<const uint32_t*>(ex[1][0])[p];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) u = pick2<KT, false>(u, reinterpret_cast<const uint32_t*>(ex[1][w])[p]);
+    }
+    const float2 f = KT == KCA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
+                                   : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+    v[0] = f.x;
+    v[1] = f.y;
   }
-  float am = max_nan(fabsf(h), fabsf(l));
+  float am = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, o));
   if (lane == 0) am_s[warp] = am;
@@ -108,8 +156,14 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SummaryArgs a) {
   for (int w = 0; w < 8; ++w) am = max_nan(am, am_s[w]);
   const float sx = am * (1.0f / 127.0f);
   const int64_t row = (int64_t)b * a.n_blocks + j;
-  a.codes[row * kCodeRow + t] = (signed char)block_code(h, sx);
-  a.codes[row * kCodeRow + kDim + t] = (signed char)block_code(l, sx);
+  signed char* out = a.codes + row * kCodeRow;
+  const uint32_t c0 = block_code(v[0], sx), c1 = block_code(v[1], sx);
+  if (KT == KCA_F32) {
+    out[t] = (signed char)c0;
+    out[kDim + t] = (signed char)c1;
+  } else {   // hi's 128 pairs, then lo's
+    *reinterpret_cast<unsigned short*>(out + 2 * t) = (unsigned short)(c0 | (c1 << 8));
+  }
   if (t == 0) a.scales[row] = sx;
 }
 
@@ -124,14 +178,19 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SummaryArgs a) {
 // 16-byte pieces, and the codes go from memory to the MMA without passing
 // through shared memory.
 // Choice: the CTA that draws a sequence's last ticket (nothing waits) holds
-// all its scores, eight per thread, as ordered 32-bit keys; a radix search
-// over the four bytes finds the smallest key taken, and two counts in index
-// order place the blocks.
+// all its scores, eight per thread, as ordered 32-bit keys.  A histogram of
+// 2,048 bins over the span of the keys (not over their leading bits, which
+// scores share: their counts would all meet in a few words) finds the bin of
+// the smallest key taken; the search goes on inside that bin until it is
+// taken whole or holds one value -- one or two rounds for scores that differ.
+// Two counts in index order place the blocks.
 // Bound: latency (516 bytes a block: 1 MB for 131,072 keys), hence many small
 // CTAs and one launch.
 constexpr int kSelThreads = 256;
 constexpr int kSelBlocks = 64;                       // blocks scored per CTA
-constexpr int kSelPer = KCA_MAX_BLOCKS / kSelThreads;  // scores per thread in the choice
+constexpr int kSelPer = KCA_MAX_BLOCKS / kSelThreads;  // scores per thread in the choice, and bins
+constexpr int kSelBinBits = 11;
+static_assert((1 << kSelBinBits) == kSelThreads * kSelPer, "thread t owns bins 8 t .. 8 t + 7");
 static_assert(kSelPer == 8, "two 16-byte loads of scores per thread");
 
 struct SelectArgs {
@@ -166,13 +225,15 @@ template <int QT>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
   __shared__ __align__(16) unsigned char qc[kHeads * kDim];   // query codes
   __shared__ float sq_s[kHeads];
-  __shared__ int hist[4][256];
+  __shared__ __align__(16) int hist[1 << kSelBinBits];
+  __shared__ uint32_t wlo[8], whi[8];
+  __shared__ int found[3];
   __shared__ int warp_sum[8];
   __shared__ int last;
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tig = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) hist[i][threadIdx.x] = 0;
+  reinterpret_cast<int4*>(hist)[2 * threadIdx.x] = make_int4(0, 0, 0, 0);
+  reinterpret_cast<int4*>(hist)[2 * threadIdx.x + 1] = make_int4(0, 0, 0, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int64_t ctx = a.ctx[b];
@@ -271,24 +332,49 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
       key[i] = j >= nb ? 0u : (j < a.n_sink || j >= nb - a.n_recent) ? 0xffffffffu : order_key(s[i]);
     }
   }
-  // Radix search, highest byte first: `want` keys are still to be taken among
-  // those that share `prefix`; the bin that holds the want-th largest extends
-  // the prefix.  Every warp scans the bins itself (lane l: bins 8 l .. 8 l + 7).
-  uint32_t prefix = 0;
-  int want = k;
+  // The span of the keys that are chosen by score.  The forced ones (all
+  // above it) are taken anyway: more blocks than n_select exist here, so the
+  // first n_sink and the last n_recent are distinct.
+  uint32_t lo_k = 0xffffffffu, hi_k = 0u;
 #pragma unroll
-  for (int pass = 0; pass < 4; ++pass) {
-    const int sh = 24 - 8 * pass;
+  for (int i = 0; i < kSelPer; ++i) {
+    const uint32_t x = key[i];
+    if (threadIdx.x * kSelPer + i >= nb || x == 0xffffffffu) continue;
+    lo_k = min(lo_k, x);
+    hi_k = max(hi_k, x);
+  }
+  lo_k = __reduce_min_sync(0xffffffffu, lo_k);
+  hi_k = __reduce_max_sync(0xffffffffu, hi_k);
+  if (lane == 0) {
+    wlo[warp] = lo_k;
+    whi[warp] = hi_k;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    lo_k = min(lo_k, wlo[w]);
+    hi_k = max(hi_k, whi[w]);
+  }
+  // `want` keys are still to be taken among those in [lo_k, hi_k]; those above
+  // are taken.  At the end `prefix` is the smallest key of which any is taken
+  // (want of them, by index), or one below it (want 0).
+  int want = k - a.n_sink - a.n_recent;
+  uint32_t prefix = 0xfffffffeu;
+  while (want > 0) {   // at most three rounds: 11 bits of the span each
+    const int bits = 32 - __clz(hi_k - lo_k);
+    if (bits == 0) {   // one value is left
+      prefix = lo_k;
+      break;
+    }
+    const int sh = bits > kSelBinBits ? bits - kSelBinBits : 0;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i)
-      if (threadIdx.x * kSelPer + i < nb && (pass == 0 || (key[i] >> (sh + 8)) == prefix))
-        atomicAdd(&hist[pass][(key[i] >> sh) & 0xffu], 1);
+      if (threadIdx.x * kSelPer + i < nb && key[i] >= lo_k && key[i] <= hi_k) atomicAdd(&hist[(key[i] - lo_k) >> sh], 1);
     __syncthreads();
-    int h[8], sum = 0;
-    const int4 h0 = *reinterpret_cast<const int4*>(&hist[pass][8 * lane]);
-    const int4 h1 = *reinterpret_cast<const int4*>(&hist[pass][8 * lane + 4]);
-    h[0] = h0.x; h[1] = h0.y; h[2] = h0.z; h[3] = h0.w;
-    h[4] = h1.x; h[5] = h1.y; h[6] = h1.z; h[7] = h1.w;
+    const int4 h0 = reinterpret_cast<const int4*>(hist)[2 * threadIdx.x];
+    const int4 h1 = reinterpret_cast<const int4*>(hist)[2 * threadIdx.x + 1];
+    const int h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+    int sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += h[i];
     int above = sum;   // keys in the bins of this lane and of higher lanes
@@ -297,20 +383,32 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
       const int v = __shfl_down_sync(0xffffffffu, above, o);
       if (lane + o < 32) above += v;
     }
-    above -= sum;      // in bins above this lane's
-    int bin = -1, rest = 0;
+    if (lane == 0) warp_sum[warp] = above;
+    // ready for the next round: this thread alone reads these bins
+    reinterpret_cast<int4*>(hist)[2 * threadIdx.x] = make_int4(0, 0, 0, 0);
+    reinterpret_cast<int4*>(hist)[2 * threadIdx.x + 1] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    above -= sum;
+    for (int w = warp + 1; w < 8; ++w) above += warp_sum[w];
+    if (above < want && above + sum >= want) {   // exactly one thread
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      if (bin < 0 && above < want && above + h[i] >= want) {
-        bin = 8 * lane + i;
-        rest = want - above;
+      for (int i = 7; i >= 0; --i) {
+        if (above < want && above + h[i] >= want) {
+          found[0] = 8 * threadIdx.x + i;
+          found[1] = want - above;
+          found[2] = h[i];
+        }
+        above += h[i];
       }
-      above += h[i];
     }
-    const unsigned who = __ballot_sync(0xffffffffu, bin >= 0);   // exactly one lane
-    const int src = __ffs(who) - 1;
-    prefix = (prefix << 8) | (uint32_t)__shfl_sync(0xffffffffu, bin, src);
-    want = __shfl_sync(0xffffffffu, rest, src);
+    __syncthreads();
+    lo_k += (uint32_t)found[0] << sh;
+    hi_k = min(hi_k, lo_k + ((1u << sh) - 1u));
+    want = found[1];
+    if (want == found[2]) {   // the whole bin is taken (no key is 0)
+      prefix = lo_k - 1u;
+      want = 0;
+    }
   }
   // Taken: every key above `prefix`, and of the keys equal to it the first
   // `want` by index.  Places by a scan in index order of both counts (16 bits

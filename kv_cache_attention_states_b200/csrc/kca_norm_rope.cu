@@ -102,11 +102,24 @@ __device__ __forceinline__ void put4(int dt, void* row, int dim, const float* x)
   *reinterpret_cast<uint2*>(static_cast<unsigned short*>(row) + dim) = make_uint2(w[0], w[1]);
 }
 
+// Weight and offset of a lane's eight dims: 1 where there is no weight.
+__device__ __forceinline__ void row_weight(const NormRopeArgs& a, const void* w, int d1, int d2, float (&wt)[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wt[j] = 1.f;
+    return;
+  }
+  get4(a.w_dtype, w, d1, wt);
+  get4(a.w_dtype, w, d2, wt + 4);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) wt[j] += a.w0;
+}
+
 // Lane l of a warp holds dims 4 l .. 4 l + 3 and 128 + 4 l .. + 3 of each of
 // its rows: the two halves of four rotation pairs, and 256- or 512-byte
 // contiguous accesses per warp.
 template <int IT, int HG>
-__global__ void __launch_bounds__(kNormWarps * 32) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kNormWarps * 32, HG == 1 ? 1 : 4) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int kGroups = kTokenRows / HG;
   constexpr int kIn = ElemBytes<IT>::value;
   const int64_t w = (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
@@ -150,35 +163,37 @@ __global__ void __launch_bounds__(kNormWarps * 32) norm_rope_kernel(const __grid
       sincospif(2.f * (float)t, &s[i], &c[i]);
     }
   }
+  // Sums of squares of the warp's rows, then 1 / sqrt(mean + eps).
+  float rs[HG];
+#pragma unroll
+  for (int i = 0; i < HG; ++i) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
+    rs[i] = ss;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < HG; ++i) rs[i] += __shfl_xor_sync(0xffffffffu, rs[i], o);
+  float wt[8];   // the warp's query rows share one weight, read once
+  if (a.norm_qk && first < kHeads) row_weight(a, a.wq, d1, d2, wt);
 #pragma unroll
   for (int i = 0; i < HG; ++i) {
     const int r = first + i;
     if (r < kTokenRows - 1 ? a.norm_qk : a.norm_v) {
-      float ss = 0.f;
+      if (r == kHeads) row_weight(a, a.wk, d1, d2, wt);
+      const float f = 1.f / sqrtf(rs[i] * (1.f / kDim) + a.eps);
+      const bool weighted = r < kTokenRows - 1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float rs = 1.f / sqrtf(ss * (1.f / kDim) + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] *= rs;
-      const void* wp = r < kHeads ? a.wq : r == kHeads ? a.wk : nullptr;
-      if (wp != nullptr) {
-        float wt[8];
-        get4(a.w_dtype, wp, d1, wt);
-        get4(a.w_dtype, wp, d2, wt + 4);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] *= wt[j] + a.w0;
-      }
+      for (int j = 0; j < 8; ++j) x[i][j] = weighted ? x[i][j] * f * wt[j] : x[i][j] * f;
     }
-    if (r <= kHeads) {
-      if (turn) {
+    if (r <= kHeads && turn) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = x[i][j], hi = x[i][4 + j];
-          x[i][j] = lo * c[j] - hi * s[j];
-          x[i][4 + j] = hi * c[j] + lo * s[j];
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float lo = x[i][j], hi = x[i][4 + j];
+        x[i][j] = lo * c[j] - hi * s[j];
+        x[i][4 + j] = hi * c[j] + lo * s[j];
       }
     }
     const int dt = r < kHeads ? a.q_dtype : a.kv_dtype;
