@@ -10,7 +10,6 @@ library raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -192,20 +191,34 @@ def _check(status: int, what: str):
         raise KcaError(status, what)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on(device):
-    """The library works on the current device: makes `device` it for a call."""
+def _run(index: int, what: str, stream, *args):
+    """Calls entry point `what` on device `index` (the library works on the
+    current device) with the given arguments and the cudaStream_t of `stream`
+    (None: torch's current one), and raises on a status other than KCA_OK."""
     import torch
-    return _SAME_DEVICE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    C = torch._C
+    s = C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    f = getattr(_lib or lib(), what)
+    if C._cuda_getDevice() == index:
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, s)
+    if st != 0:
+        raise KcaError(st, what)
 
 
 def _need(device, **tensors):
-    """Each tensor (None is skipped) contiguous and on the CUDA device `device`."""
+    """Names the tensor (None is skipped) that is not contiguous on `device`.
+    The calls test all of theirs in one condition and come here when it fails."""
     for name, t in tensors.items():
         if t is not None and (t.device != device or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous tensor on {device}")
+
+
+def _off(t, index: int) -> bool:
+    """Whether t is anything but contiguous on device `index` (None: no)."""
+    return t is not None and (t.get_device() != index or not t.is_contiguous())
 
 
 def _ptr(t):
@@ -497,18 +510,18 @@ _FREQ_AXIS = {}
 
 
 def _freq_axis(freq_axis, n_axes: int):
-    """The axis of each of the 128 frequencies as a C byte array (made once
-    per distinct assignment), or None."""
+    """The axis of each of the 128 frequencies as a C byte array (checked and
+    made once per distinct assignment), or None."""
     if freq_axis is None:
         return None
     key = bytes(freq_axis)
-    if len(key) != HEAD_DIM // 2 or max(key) >= n_axes:
-        raise ValueError(f"freq_axis must give one of {n_axes} axes for each of 128 frequencies")
-    arr = _FREQ_AXIS.get(key)
+    arr = _FREQ_AXIS.get((key, n_axes))
     if arr is None:
+        if len(key) != HEAD_DIM // 2 or max(key) >= n_axes:
+            raise ValueError(f"freq_axis must give one of {n_axes} axes for each of 128 frequencies")
         if len(_FREQ_AXIS) >= 64:
             _FREQ_AXIS.clear()
-        arr = _FREQ_AXIS[key] = (ctypes.c_uint8 * len(key)).from_buffer_copy(key)
+        arr = _FREQ_AXIS[key, n_axes] = (ctypes.c_uint8 * len(key)).from_buffer_copy(key)
     return arr
 
 
@@ -529,70 +542,101 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
     of the cache's), or q itself.
     """
     import torch
-    n, dev = q.shape[0], q.device
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if q.shape[1:] != (N_Q_HEADS, HEAD_DIM) or q.stride(2) != 1 or q.stride(1) != HEAD_DIM:
+    shape, q_stride = q.shape, q.stride()
+    n = shape[0]
+    if shape != (n, N_Q_HEADS, HEAD_DIM) or q_stride[2] != 1 or q_stride[1] != HEAD_DIM:
         raise ValueError("q must be [n, 8, 256] with each token's values contiguous")
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if (t.device != dev or t.dtype != q.dtype or t.shape[0] != n or t.shape[-1] != HEAD_DIM
-                or (t.dim() != 2 and (t.dim() != 3 or t.shape[1] != 1)) or t.stride(-1) != 1):
-            raise ValueError(f"{name} must be [n, 256] of q's dtype on {dev}, each token's values contiguous")
-    _need(dev, k_cache=k_cache, v_cache=v_cache, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
-          k_weight=k_weight, q_out=q_out, workspace=workspace)
-    if k_cache.dtype != v_cache.dtype or k_cache.shape[-1] != HEAD_DIM or v_cache.numel() != k_cache.numel():
+    in_dtype, row, row1 = q.dtype, (n, HEAD_DIM), (n, 1, HEAD_DIM)
+    k_stride, v_stride = k_new.stride(), v_new.stride()
+    for name, t, st in (("k_new", k_new, k_stride), ("v_new", v_new, v_stride)):
+        shape = t.shape
+        if t.get_device() != dev or t.dtype is not in_dtype or (shape != row and shape != row1) or st[-1] != 1:
+            raise ValueError(f"{name} must be [n, 256] of q's dtype on {q.device}, each token's values contiguous")
+    if (k_cache.get_device() != dev or not k_cache.is_contiguous() or v_cache.get_device() != dev
+            or not v_cache.is_contiguous() or _off(positions, dev) or _off(inv_freq, dev) or _off(q_weight, dev)
+            or _off(k_weight, dev) or _off(q_out, dev) or _off(workspace, dev)):
+        _need(q.device, k_cache=k_cache, v_cache=v_cache, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+              k_weight=k_weight, q_out=q_out, workspace=workspace)
+    shape = k_cache.shape
+    if shape != v_cache.shape or shape[-1] != HEAD_DIM or k_cache.dtype is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must be alike, with a last axis of 256")
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("give both positions and inv_freq, or neither")
-    n_axes = 1
+    n_axes, pos_p, inv_p = 1, None, None
     if positions is not None:
-        n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dtype != torch.int64 or positions.dim() > 2 or positions.numel() != n_axes * n or positions.shape[-1] != n:
+        if inv_freq is None:
+            raise ValueError("give both positions and inv_freq, or neither")
+        shape = positions.shape
+        if len(shape) == 2:
+            n_axes = shape[0]
+        if positions.dtype is not torch.int64 or (shape != (n_axes, n) and shape != (n,)):
             raise ValueError("positions must be int64 [n] or [axes, n]")
-        if inv_freq.dtype != torch.float32 or inv_freq.numel() != HEAD_DIM // 2:
+        if inv_freq.dtype is not torch.float32 or inv_freq.numel() != HEAD_DIM // 2:
             raise ValueError("inv_freq must be float32 [128]")
-    wt = q_weight if q_weight is not None else k_weight
-    for t in (q_weight, k_weight):
-        if t is not None and (t.numel() != HEAD_DIM or t.dtype != wt.dtype):
+        pos_p, inv_p = positions.data_ptr(), inv_freq.data_ptr()
+    elif inv_freq is not None:
+        raise ValueError("give both positions and inv_freq, or neither")
+    wt = k_weight if q_weight is None else q_weight
+    wq_p = wk_p = None
+    if q_weight is not None:
+        if q_weight.numel() != HEAD_DIM:
+            raise ValueError("q_weight must be [256]")
+        wq_p = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.numel() != HEAD_DIM or k_weight.dtype is not wt.dtype:
             raise ValueError("q_weight and k_weight must be [256] of one dtype")
+        wk_p = k_weight.data_ptr()
     if q_out is None:
-        q_out = torch.empty((n, N_Q_HEADS, HEAD_DIM), dtype=k_cache.dtype, device=dev)
-    if q_out.numel() != n * N_Q_HEADS * HEAD_DIM:
+        q_out = torch.empty((n, N_Q_HEADS, HEAD_DIM), dtype=k_cache.dtype, device=q.device)
+    elif q_out.numel() != n * N_Q_HEADS * HEAD_DIM:
         raise ValueError("q_out must be [n, 8, 256]")
     if isinstance(dst, int):
         dst_p, dst0 = None, dst
     else:
-        if dst.dtype != torch.int64 or dst.device != dev or dst.numel() != n or not dst.is_contiguous():
+        if dst.dtype is not torch.int64 or dst.numel() != n or _off(dst, dev):
             raise ValueError("dst must be an int or a contiguous int64 CUDA tensor [n]")
         dst_p, dst0 = dst.data_ptr(), 0
-    with _on(dev):
-        st = lib().attn_norm_rope_append(
-            q.data_ptr(), q.stride(0), k_new.data_ptr(), k_new.stride(0), v_new.data_ptr(), v_new.stride(0),
-            dtype_code(q), n, (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), _ptr(q_weight), _ptr(k_weight),
-            F32 if wt is None else dtype_code(wt), weight_offset, eps, _ptr(positions), n_axes,
-            _freq_axis(freq_axis, n_axes), _ptr(inv_freq), q_out.data_ptr(), dtype_code(q_out), k_cache.data_ptr(),
-            v_cache.data_ptr(), dtype_code(k_cache), k_cache.numel() // HEAD_DIM, dst_p, dst0, _ptr(workspace),
-            _stream_ptr(stream, dev))
-    _check(st, "attn_norm_rope_append")
+    _run(dev, "attn_norm_rope_append", stream, q.data_ptr(), q_stride[0], k_new.data_ptr(), k_stride[0],
+         v_new.data_ptr(), v_stride[0], dtype_code(q), n, (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), wq_p,
+         wk_p, F32 if wt is None else dtype_code(wt), weight_offset, eps, pos_p, n_axes, _freq_axis(freq_axis, n_axes),
+         inv_p, q_out.data_ptr(), dtype_code(q_out), k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache),
+         k_cache.numel() // HEAD_DIM, dst_p, dst0, _ptr(workspace))
     return q_out
 
 
 # ------------------------------------------------------ shared-prefix decode
 
-def _out_dtype(q, out, shape):
-    """`out`, or a new float32 tensor of `shape`, and its dtype code."""
+def _out_dtype(q, out):
+    """`out`, or a new float32 tensor of q's shape, and its dtype code."""
     import torch
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
-    if out.numel() != q.numel() or (out.dtype != torch.float32 and out.dtype != q.dtype):
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    elif out.numel() != q.numel() or (out.dtype != q.dtype and out.dtype is not torch.float32):
         raise ValueError("out must have q's shape and be float32 or of q's dtype")
     return out, dtype_code(out)
 
 
 def _device_lengths(ctx_len_dev, batch: int):
     import torch
-    if ctx_len_dev.dtype != torch.int64 or ctx_len_dev.numel() != batch:
+    if ctx_len_dev.dtype is not torch.int64 or ctx_len_dev.numel() != batch:
         raise ValueError("ctx_len_dev must be int64 with one entry per sequence")
+
+
+def _queries(q) -> int:
+    """Batch of decode queries [batch, 8, 256]; q's device is checked elsewhere."""
+    batch = q.shape[0]
+    if q.numel() != batch * N_Q_HEADS * HEAD_DIM:
+        raise ValueError("q must be [batch, 8, 256]")
+    return batch
+
+
+def _cache_shape(k_cache, v_cache, batch: int) -> int:
+    """Capacity of a batched cache [batch, capacity, 256] (or [.., 1, 256])."""
+    shape = k_cache.shape
+    if shape[0] != batch or v_cache.shape != shape or k_cache.numel() != batch * shape[1] * HEAD_DIM:
+        raise ValueError("q, k_cache and v_cache must agree in batch and shape, [batch, capacity, 256]")
+    return shape[1]
 
 
 def attn_decode_prefix_workspace_bytes(q_dtype: int, kv_dtype: int, prefix_len: int, ctx_len, window: int = 0) -> int:
@@ -616,24 +660,28 @@ def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache,
     float32 (the default) or of q's dtype.  Returns out [batch, 8, 256].
     """
     import torch
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    batch, dev = q.shape[0], q.device
-    on_device = isinstance(ctx_len, torch.Tensor) and ctx_len.is_cuda
-    _need(dev, q=q, prefix_k=prefix_k, prefix_v=prefix_v, k_cache=k_cache, v_cache=v_cache, out=out,
-          workspace=workspace, ctx_len=ctx_len if on_device else None)
-    if k_cache.shape[0] != batch or v_cache.shape != k_cache.shape or q.numel() != batch * N_Q_HEADS * HEAD_DIM:
-        raise ValueError("q, k_cache and v_cache must agree in batch and shape")
+    batch = _queries(q)
+    on_device = hasattr(ctx_len, "is_cuda") and ctx_len.is_cuda
+    if (_off(q, dev) or _off(prefix_k, dev) or _off(prefix_v, dev) or _off(k_cache, dev) or _off(v_cache, dev)
+            or _off(out, dev) or _off(workspace, dev) or (on_device and _off(ctx_len, dev))):
+        _need(q.device, q=q, prefix_k=prefix_k, prefix_v=prefix_v, k_cache=k_cache, v_cache=v_cache, out=out,
+              workspace=workspace, ctx_len=ctx_len if on_device else None)
+    capacity = _cache_shape(k_cache, v_cache, batch)
     if prefix_len > 0 and (prefix_k is None or prefix_v is None):
         raise ValueError("a prefix of more than 0 rows needs prefix_k and prefix_v")
-    for t in (prefix_k, prefix_v, v_cache):
-        if t is not None and t.dtype != k_cache.dtype:
-            raise TypeError("the prefix and the caches must share a dtype")
+    kv = k_cache.dtype
+    if v_cache.dtype != kv:
+        raise TypeError("the prefix and the caches must share a dtype")
     for t in (prefix_k, prefix_v):
-        if t is not None and t.numel() < prefix_len * HEAD_DIM:
-            raise ValueError("the prefix has fewer than prefix_len rows")
-    capacity = k_cache.shape[1]
-    out, od = _out_dtype(q, out, (batch, N_Q_HEADS, HEAD_DIM))
+        if t is not None:
+            if t.dtype != kv:
+                raise TypeError("the prefix and the caches must share a dtype")
+            if t.numel() < prefix_len * HEAD_DIM:
+                raise ValueError("the prefix has fewer than prefix_len rows")
+    out, od = _out_dtype(q, out)
     qd, kd = dtype_code(q), dtype_code(k_cache)
     if on_device:
         _device_lengths(ctx_len, batch)
@@ -645,15 +693,13 @@ def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache,
         if nctx != batch:
             raise ValueError("ctx_len must have one entry per sequence")
         dev_p, ctx_bound = None, 0
-    with _on(dev):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             workspace = new_workspace(attn_decode_prefix_workspace_bytes(
-                qd, kd, prefix_len, [ctx_bound] * batch if on_device else ctx_len, window), dev, stream)
-        st = lib().attn_decode_prefix(q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(),
-                                      v_cache.data_ptr(), kd, N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p,
-                                      dev_p, ctx_bound, window, scale, out.data_ptr(), od, workspace.data_ptr(),
-                                      workspace.numel(), _stream_ptr(stream, dev))
-    _check(st, "attn_decode_prefix")
+                qd, kd, prefix_len, [ctx_bound] * batch if on_device else ctx_len, window), q.device, stream)
+    _run(dev, "attn_decode_prefix", stream, q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(),
+         v_cache.data_ptr(), kd, N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p, dev_p, ctx_bound, window, scale,
+         out.data_ptr(), od, workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -668,27 +714,26 @@ def attn_summarize_blocks(k_cache, ctx_len_dev, n_new: int, codes=None, scales=N
     other blocks stay as they are.  Returns codes, scales.
     """
     import torch
-    if not k_cache.is_cuda:
+    dev = k_cache.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    batch, capacity, dev = k_cache.shape[0], k_cache.shape[1], k_cache.device
+    batch, capacity = k_cache.shape[:2]
     blocks = -(-capacity // BLOCK_KEYS)
     if codes is None:
-        codes = torch.zeros((batch, blocks, 2, HEAD_DIM), dtype=torch.int8, device=dev)
+        codes = torch.zeros((batch, blocks, 2, HEAD_DIM), dtype=torch.int8, device=k_cache.device)
     if scales is None:
-        scales = torch.zeros((batch, blocks), dtype=torch.float32, device=dev)
-    _need(dev, k_cache=k_cache, ctx_len_dev=ctx_len_dev, codes=codes, scales=scales, workspace=workspace)
+        scales = torch.zeros((batch, blocks), dtype=torch.float32, device=k_cache.device)
+    if (_off(k_cache, dev) or _off(ctx_len_dev, dev) or _off(codes, dev) or _off(scales, dev) or _off(workspace, dev)):
+        _need(k_cache.device, k_cache=k_cache, ctx_len_dev=ctx_len_dev, codes=codes, scales=scales, workspace=workspace)
     _device_lengths(ctx_len_dev, batch)
     if k_cache.numel() != batch * capacity * HEAD_DIM:
         raise ValueError("k_cache must be [batch, capacity, 256]")
-    if codes.dtype != torch.int8 or codes.numel() != batch * blocks * 2 * HEAD_DIM:
+    if codes.dtype is not torch.int8 or codes.numel() != batch * blocks * 2 * HEAD_DIM:
         raise ValueError("codes must be int8 [batch, ceil(capacity / 64), 2, 256]")
-    if scales.dtype != torch.float32 or scales.numel() != batch * blocks:
+    if scales.dtype is not torch.float32 or scales.numel() != batch * blocks:
         raise ValueError("scales must be float32 [batch, ceil(capacity / 64)]")
-    with _on(dev):
-        st = lib().attn_summarize_blocks(k_cache.data_ptr(), dtype_code(k_cache), capacity, batch,
-                                         ctx_len_dev.data_ptr(), n_new, codes.data_ptr(), scales.data_ptr(),
-                                         _ptr(workspace), _stream_ptr(stream, dev))
-    _check(st, "attn_summarize_blocks")
+    _run(dev, "attn_summarize_blocks", stream, k_cache.data_ptr(), dtype_code(k_cache), capacity, batch, ctx_len_dev.data_ptr(),
+         n_new, codes.data_ptr(), scales.data_ptr(), _ptr(workspace))
     return codes, scales
 
 
@@ -709,28 +754,28 @@ def attn_select_blocks(q, codes, scales, ctx_len_dev, ctx_bound: int, n_select: 
     [batch, n_select], ascending, -1 behind the last.
     """
     import torch
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    batch, dev = q.shape[0], q.device
+    batch = _queries(q)
     if blocks is None:
-        blocks = torch.empty((batch, n_select), dtype=torch.int32, device=dev)
-    _need(dev, q=q, codes=codes, scales=scales, ctx_len_dev=ctx_len_dev, blocks=blocks, workspace=workspace)
+        blocks = torch.empty((batch, n_select), dtype=torch.int32, device=q.device)
+    if (_off(q, dev) or _off(codes, dev) or _off(scales, dev) or _off(ctx_len_dev, dev) or _off(blocks, dev)
+            or _off(workspace, dev)):
+        _need(q.device, q=q, codes=codes, scales=scales, ctx_len_dev=ctx_len_dev, blocks=blocks, workspace=workspace)
     _device_lengths(ctx_len_dev, batch)
-    if q.numel() != batch * N_Q_HEADS * HEAD_DIM:
-        raise ValueError("q must be [batch, 8, 256]")
-    if (codes.dtype != torch.int8 or scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != batch
+    shape = scales.shape
+    if (codes.dtype is not torch.int8 or scales.dtype is not torch.float32 or len(shape) != 2 or shape[0] != batch
             or codes.numel() != scales.numel() * 2 * HEAD_DIM):
         raise ValueError("codes must be int8 [batch, blocks, 2, 256] and scales float32 [batch, blocks]")
-    if blocks.dtype != torch.int32 or blocks.numel() != batch * n_select:
+    if blocks.dtype is not torch.int32 or blocks.numel() != batch * n_select:
         raise ValueError("blocks must be int32 [batch, n_select]")
-    with _on(dev):
-        if workspace is None:
-            workspace = new_workspace(attn_select_blocks_workspace_bytes(batch, ctx_bound), dev, stream)
-        st = lib().attn_select_blocks(q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), scales.shape[1],
-                                      batch, ctx_len_dev.data_ptr(), ctx_bound, n_select, n_sink, n_recent,
-                                      blocks.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                      _stream_ptr(stream, dev))
-    _check(st, "attn_select_blocks")
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = new_workspace(attn_select_blocks_workspace_bytes(batch, ctx_bound), q.device, stream)
+    _run(dev, "attn_select_blocks", stream, q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), shape[1],
+         batch, ctx_len_dev.data_ptr(), ctx_bound, n_select, n_sink, n_recent, blocks.data_ptr(), workspace.data_ptr(),
+         workspace.numel())
     return blocks
 
 
@@ -751,28 +796,29 @@ def attn_decode_blocks(q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound: int,
     Returns out [batch, 8, 256].
     """
     import torch
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    batch, dev = q.shape[0], q.device
-    _need(dev, q=q, k_cache=k_cache, v_cache=v_cache, blocks=blocks, ctx_len_dev=ctx_len_dev, out=out,
-          workspace=workspace)
+    batch = _queries(q)
+    if (_off(q, dev) or _off(k_cache, dev) or _off(v_cache, dev) or _off(blocks, dev) or _off(ctx_len_dev, dev)
+            or _off(out, dev) or _off(workspace, dev)):
+        _need(q.device, q=q, k_cache=k_cache, v_cache=v_cache, blocks=blocks, ctx_len_dev=ctx_len_dev, out=out,
+              workspace=workspace)
     _device_lengths(ctx_len_dev, batch)
-    if k_cache.shape[0] != batch or v_cache.shape != k_cache.shape or q.numel() != batch * N_Q_HEADS * HEAD_DIM:
-        raise ValueError("q, k_cache and v_cache must agree in batch and shape")
-    if k_cache.dtype != v_cache.dtype:
+    capacity = _cache_shape(k_cache, v_cache, batch)
+    if k_cache.dtype is not v_cache.dtype:
         raise TypeError("k_cache and v_cache must share a dtype")
-    if blocks.dtype != torch.int32 or blocks.dim() != 2 or blocks.shape[0] != batch:
+    shape = blocks.shape
+    if blocks.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch:
         raise ValueError("blocks must be int32 [batch, n_list]")
-    out, od = _out_dtype(q, out, (batch, N_Q_HEADS, HEAD_DIM))
-    with _on(dev):
-        if workspace is None:
-            workspace = new_workspace(attn_decode_blocks_workspace_bytes(batch, blocks.shape[1]), dev, stream)
-        st = lib().attn_decode_blocks(q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
-                                      dtype_code(k_cache), N_Q_HEADS, N_KV_HEADS, HEAD_DIM, k_cache.shape[1], batch,
-                                      blocks.data_ptr(), blocks.shape[1], ctx_len_dev.data_ptr(), ctx_bound, scale,
-                                      out.data_ptr(), od, workspace.data_ptr(), workspace.numel(),
-                                      _stream_ptr(stream, dev))
-    _check(st, "attn_decode_blocks")
+    n_list = shape[1]
+    out, od = _out_dtype(q, out)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = new_workspace(attn_decode_blocks_workspace_bytes(batch, n_list), q.device, stream)
+    _run(dev, "attn_decode_blocks", stream, q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
+         dtype_code(k_cache), N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, blocks.data_ptr(), n_list,
+         ctx_len_dev.data_ptr(), ctx_bound, scale, out.data_ptr(), od, workspace.data_ptr(), workspace.numel())
     return out
 
 
