@@ -484,17 +484,22 @@ int attn_norm_rope_append(const void *q, int64_t q_stride, const void *k_new, in
  *                2, detail (10 << 24) | sequence).  Give exactly one of the two.
  *   window, scale  as in attn_decode: positions [ctx-window, ctx-1] are seen
  *   out          [batch][8][256] of out_dtype, which is F32 or q_dtype
- *   workspace    >= attn_decode_prefix_workspace_bytes(...) bytes; with
- *                ctx_len_dev, ask for ctx_len = {ctx_bound, ...}
- * q_dtype == kv_dtype in {F16, BF16} and 3 or more sequences take the
- * tensor-core prefill kernel for the prefix, whose probabilities are rounded to
+ *   workspace    >= attn_decode_prefix_workspace_bytes(...) bytes of these
+ *                lengths, or of any whose longest is no shorter: a caller whose
+ *                sequences grow asks once for ctx_len = {ctx_bound, ...}, as
+ *                one with ctx_len_dev does
+ * Short work -- f32 caches always -- runs in the decode kernels, each sequence
+ * over prefix and own keys (one launch; f32 caches two), f32-grade.  Where one
+ * pass over the prefix for all sequences is estimated to be faster, it is
+ * computed first: with q_dtype == kv_dtype in {F16, BF16} by the tensor-core
+ * prefill kernel, 16 sequences a row tile, whose probabilities are rounded to
  * kv_dtype before the V product (as in attn_prefill: the relative error of a
- * 16-bit rounding, whatever out_dtype).  Other 16-bit caches take multi-row
- * units, f32 caches and single sequences the decode kernels, all f32-grade; the
- * sequences' own keys take the kernels of attn_decode_partial.  With a 16-bit
- * cache and 2 or more sequences, V must be finite on the prefix rows from
- * prefix_len - window (0 without a window) on: a masked key's probability is 0,
- * and 0 times an infinity is not.
+ * 16-bit rounding, whatever out_dtype); with any other 16-bit cache in
+ * multi-row units, f32-grade.  V must then be finite on the prefix rows from
+ * prefix_len - window (0 without a window) on: a masked key's probability is
+ * 0, and 0 times an infinity is not.  attn_force_path's op 0 pins the form
+ * (16-bit caches): 0 the decode kernels, 1 tiles where they are possible, else
+ * units, 2 units.
  * A sequence that sees no key gives zeros.
  * Everything else is as in attn_decode.
  */

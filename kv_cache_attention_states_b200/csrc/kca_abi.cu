@@ -305,9 +305,9 @@ int prefill_route(int32_t q_dtype, int32_t kv_dtype, int64_t chunk_start, int32_
 // 1.5 us (partials, fence, ticket) and 0.6 us per round of loads of the
 // final merge.
 // capacity: resident clusters of 2, 4 and 8 CTAs (nullptr: the current
-// device's, measured once per device).
+// device's, measured once per device).  seconds: the estimate.
 kca::RowsPlan mma_rows_plan(int32_t n_units, const int64_t* nkeys, int sms, int* cluster,
-                            const int32_t* capacity = nullptr) {
+                            const int32_t* capacity = nullptr, double* seconds = nullptr) {
   kca::RowsPlan best{};
   int best_c = 0;
   double best_t = 0.0;
@@ -335,6 +335,7 @@ kca::RowsPlan mma_rows_plan(int32_t n_units, const int64_t* nkeys, int sms, int*
     }
   }
   *cluster = best_c;
+  if (seconds != nullptr) *seconds = best_t;
   return best;
 }
 
@@ -374,11 +375,9 @@ kca::RowsPlan rows_plan(int32_t kv_dtype, int32_t n_units, const int64_t* nkeys,
 }
 
 // Launches the rows path: tensor cores for 16-bit caches (tensor maps over the
-// cache_rows rows of the cache), CUDA cores otherwise.  offset: where the
-// partials start in the workspace.
+// cache_rows rows of the cache), CUDA cores otherwise.
 int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, const void* v_cache,
-                     int64_t cache_rows, kca::RowsArgs a, int cluster, void* workspace, cudaStream_t s,
-                     size_t offset = KCA_WORKSPACE_HEADER) {
+                     int64_t cache_rows, kca::RowsArgs a, int cluster, void* workspace, cudaStream_t s) {
   a.cache_rows = cache_rows;
   if (use_rows_mma(kv_dtype)) {
     a.cluster = cluster;
@@ -388,7 +387,7 @@ int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, con
       // Counters live in the header (no other path writes there), cluster
       // partials where the CUDA-core path keeps its split partials.
       a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kStatusBytes);
-      carve(workspace, (size_t)a.n_units * a.max_clusters * kHeads * 2 * 4, &a.cpart_ml, &a.cpart_acc, offset);
+      carve(workspace, (size_t)a.n_units * a.max_clusters * kHeads * 2 * 4, &a.cpart_ml, &a.cpart_acc);
     }
     CUtensorMap tmk, tmv;
     if (!encode_kv_map(&tmk, k_cache, kv_dtype, 0, cache_rows, 64) ||
@@ -397,7 +396,7 @@ int launch_rows_path(int32_t q_dtype, int32_t kv_dtype, const void* k_cache, con
     return kca::launch_decode_mma(q_dtype, kv_dtype, tmk, tmv, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
   }
   a.part_slots = a.max_splits > 1 ? (int64_t)a.n_units * a.max_splits : 0;
-  carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc, offset);
+  carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc);
   return kca::launch_rows(q_dtype, kv_dtype, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
 }
 
@@ -503,66 +502,150 @@ int launch_multirow_route(const void* q, int32_t q_dtype, const void* k_cache, c
 
 // Plan of attn_decode_prefix: how the prefix is computed (route), the sequences'
 // own keys, and where everything lies in the workspace.
-//   kTc       q and cache of one 16-bit type, 3 or more sequences: the
-//             tensor-core prefill kernel, 16 sequences a row tile
-//   kUnits    another 16-bit cache, 2 or more sequences: multi-row units
-//   kRows     one sequence or an f32 cache: the decode kernels, each sequence
-//             over the whole prefix
-//   kNone     no query sees any of it
+//   kTiles   q and cache of one 16-bit type: the tensor-core prefill kernel, 16
+//            sequences a row tile, then the decode kernel over the own keys,
+//            which merges the prefix's partials
+//   kUnits   any 16-bit cache: multi-row units in its place (f32-grade)
+//   kJoined  the decode kernel over prefix and own keys of each sequence: one
+//            launch (f32 caches: and their merge), every sequence reading the
+//            prefix for itself
+constexpr int64_t kRowsStage = kca::kRowsMmaStage;   // keys of a stage of the decode kernel
 struct PrefixPlan {
-  enum Route { kNone, kTc, kUnits, kRows } route;
+  enum Route { kTiles, kUnits, kJoined } route;
   int64_t kv_lo;               // first prefix position that a query may see
-  kca::TcPlan tc;
-  kca::RowsPlan pre, own;      // kUnits / kRows; the sequences' own keys
-  int pre_cluster, own_cluster;
+  kca::TcPlan tc;              // kTiles
+  kca::RowsPlan pre;           // kUnits
   int32_t unit_rows;
-  size_t own_rec, pre_rec, pre_parts, own_parts, total;   // byte offsets; bytes
+  kca::RowsPlan own;           // the own keys, or (kJoined) all of them
+  int own_cluster;             // 0: CUDA cores
+  size_t own_parts, total;     // byte offset; bytes
 };
+size_t slots_bytes(size_t slots) { return align_up(slots * 2 * 4) + align_up(slots * kDim * 4); }
 
-// ctx: context lengths, or (dev) their bounds; KCA_OK or KCA_ERR_CUDA.
-int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t batch, const int64_t* ctx, bool dev,
-                int32_t window, PrefixPlan* out) {
+// Workspace that every plan of equal lengths fits, whatever they are: a unit
+// of such a plan gets its share of the GPU's SMs, so the partials of all units
+// are no more than one wave of CTAs writes.
+size_t prefix_ws_bound(int32_t kv_dtype, int32_t batch, int sms) {
+  size_t parts = 0;
+  if (kv_dtype != KCA_F32) {
+    const int32_t tiles = (batch + kca::kRowTile - 1) / kca::kRowTile, pairs = (tiles + 1) / 2;
+    const int32_t items = (sms / 2 > 80 ? 80 : sms / 2) / pairs;
+    parts = slots_bytes((size_t)tiles * (items < 1 ? 1 : items) * 128);
+    const int32_t ur = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
+    const int32_t splits = sms / ((batch + ur - 1) / ur);
+    const size_t units = slots_bytes((size_t)batch * (splits < 1 ? 1 : splits) * kHeads);
+    if (units > parts) parts = units;
+  }
+  return KCA_WORKSPACE_HEADER + parts + slots_bytes((size_t)(sms > batch ? sms : batch) * kHeads);
+}
+
+// lengths: context lengths, or (dev) their bounds; equal: plan as if all were
+// as long as the longest.  KCA_OK or KCA_ERR_CUDA.
+int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t batch, const int64_t* lengths, bool dev,
+                bool equal, int32_t window, PrefixPlan* out) {
   PrefixPlan p{};
+  int64_t ctx[KCA_MAX_BATCH], most = 0;
+  for (int32_t b = 0; b < batch; ++b) most = lengths[b] > most ? lengths[b] : most;
+  for (int32_t b = 0; b < batch; ++b) ctx[b] = equal ? most : lengths[b];
   int sms = 0;
   if (current_sms(&sms) != KCA_OK) return KCA_ERR_CUDA;
+  int64_t joined[KCA_MAX_BATCH], own[KCA_MAX_BATCH];   // keys of each sequence, as the kernels count them
   p.kv_lo = window > 0 ? prefix_len : 0;
-  for (int32_t b = 0; window > 0 && b < batch; ++b) {
+  for (int32_t b = 0; b < batch; ++b) {
+    int64_t lo = 0;
+    own[b] = kca::shard_visible(ctx[b] - 1, window, prefix_len, 0, &lo);
     // a device length may be as short as the prefix
-    const int64_t lo = kca::lo_of((dev ? prefix_len : ctx[b]) - 1, window);
-    if (lo < p.kv_lo) p.kv_lo = lo;
+    const int64_t first = kca::lo_of((dev ? prefix_len : lengths[b]) - 1, window);
+    if (first < p.kv_lo) p.kv_lo = first;
+    // both parts in whole stages; with a device length any cut between them
+    joined[b] = kRowsStage * (dev || equal ? kca::cdiv(kca::n_visible(ctx[b] - 1, window), kRowsStage) + 1
+                                           : kca::cdiv(kca::shard_visible(ctx[b] - 1, window, 0, prefix_len, &lo), kRowsStage) +
+                                        kca::cdiv(own[b], kRowsStage));
   }
-  const bool same16 = q_dtype == kv_dtype && kv_dtype != KCA_F32;
-  p.route = p.kv_lo >= prefix_len                  ? PrefixPlan::kNone
-            : same16 && batch >= 3                 ? PrefixPlan::kTc
-            : kv_dtype != KCA_F32 && batch >= 2    ? PrefixPlan::kUnits
-                                                   : PrefixPlan::kRows;
-  const size_t rec = align_up(sizeof(float) * KCA_PARTIAL_FLOATS((size_t)batch));
-  p.own_rec = KCA_WORKSPACE_HEADER;
-  p.pre_rec = p.own_rec + rec;
-  p.pre_parts = p.pre_rec + (p.route == PrefixPlan::kRows ? rec : 0);
-  size_t need = KCA_WORKSPACE_HEADER;   // of the prefix's partials, a header included
-  int64_t nk[KCA_MAX_BATCH], lo = 0;
-  if (p.route == PrefixPlan::kTc) {
-    p.tc = kca::make_tc_prefix_plan(p.kv_lo, prefix_len, batch, window, sms / 2);
-    need = tc_ws_bytes(p.tc);
-  } else if (p.route == PrefixPlan::kUnits) {
-    p.unit_rows = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
-    const int32_t units = (batch + p.unit_rows - 1) / p.unit_rows;
-    for (int32_t u = 0; u < units; ++u) nk[u] = prefix_len - p.kv_lo;
-    p.pre = kca::make_rows_plan(units, nk, sms, kca::kMultiRowMinSplit);
-    const size_t slots = (size_t)batch * p.pre.max_splits;
-    need += align_up(slots * kHeads * 2 * 4) + align_up(slots * kHeads * kDim * 4);
-  } else if (p.route == PrefixPlan::kRows) {
-    for (int32_t b = 0; b < batch; ++b)
-      nk[b] = dev ? prefix_len - p.kv_lo : kca::shard_visible(ctx[b] - 1, window, 0, prefix_len, &lo);
-    p.pre = rows_plan(kv_dtype, batch, nk, sms, &p.pre_cluster, &need);
-    if (p.pre_cluster < 1) return KCA_ERR_CUDA;
+  p.own_parts = KCA_WORKSPACE_HEADER;
+  if (kv_dtype == KCA_F32) {
+    p.route = PrefixPlan::kJoined;
+    p.own = kca::make_rows_plan(batch, joined, sms);
+    p.total = rows_ws_bytes(p.own);
+    *out = p;
+    return KCA_OK;
   }
-  p.own_parts = p.pre_parts + align_up(need - KCA_WORKSPACE_HEADER);
-  for (int32_t b = 0; b < batch; ++b) nk[b] = kca::shard_visible(ctx[b] - 1, window, prefix_len, 0, &lo);
-  p.own = rows_plan(kv_dtype, batch, nk, sms, &p.own_cluster, &need);
-  if (p.own_cluster < 1) return KCA_ERR_CUDA;
-  p.total = p.own_parts + align_up(need - KCA_WORKSPACE_HEADER);
+  // The routes' times in microseconds, from B200 graph replays: the decode
+  // kernel's estimate (mma_rows_plan) and 2 for a launch; or 8.5 for the
+  // tiles' and their 1.65 per 128 keys (17 and 1.1 per 64 keys for units), the
+  // own keys, and the partials' way through L2.  Measured, joined against
+  // tiles or units: 3 x 1,000 bf16 6.4 / 12.8, 8 x 8,192 of f32 queries 15.7 /
+  // 21.9, 32 x 16,384 bf16 66 / 19.3, 256 x 120,000 f16 3,389 / 204.
+  int joined_cluster = 0;
+  double t_joined = 0., t_own = 0.;
+  const kca::RowsPlan all = mma_rows_plan(batch, joined, sms, &joined_cluster, nullptr, &t_joined);
+  p.own = mma_rows_plan(batch, own, sms, &p.own_cluster, nullptr, &t_own);
+  if (joined_cluster < 1 || p.own_cluster < 1) return KCA_ERR_CUDA;
+  t_joined = 2. + 1e6 * t_joined;
+  t_own = 1e6 * t_own;
+  int64_t longest = 1;
+  for (int32_t b = 0; b < batch; ++b) longest = own[b] > longest ? own[b] : longest;
+  size_t parts = 0;
+  const int forced = g_prefill_path.load(std::memory_order_relaxed);
+  double best = 0.;
+  if (p.kv_lo < prefix_len && forced != 0) {
+    p.route = q_dtype == kv_dtype && forced != 2 ? PrefixPlan::kTiles : PrefixPlan::kUnits;
+    const kca::RowsPlan own_all = p.own;
+    const int own_all_cluster = p.own_cluster;
+    // c = 0: prefix and own keys each over the whole GPU, one after the other;
+    // else each sequence's own keys on one cluster of c CTAs beside the
+    // prefix, on SMs that it leaves (they run at once until the merge).
+    for (int c = 0; c <= 8; c = c == 0 ? 1 : 2 * c) {
+      const int left = sms - batch * c;
+      if (c > 0 && left < sms / 4) break;
+      double t = 0.;
+      size_t bytes = 0;
+      kca::TcPlan tc{};
+      kca::RowsPlan pre{};
+      int32_t ur = 0;
+      if (p.route == PrefixPlan::kTiles) {
+        tc = kca::make_tc_prefix_plan(p.kv_lo, prefix_len, batch, window, left / 2);
+        if (2 * tc.n_items > left) continue;
+        bytes = slots_bytes((size_t)tc.n_slots * 128);
+        t = 8.5 + 1.65 * tc.per_item;
+      } else {
+        ur = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
+        const int32_t units = (batch + ur - 1) / ur;
+        if (units > left) continue;
+        int64_t nk[KCA_MAX_BATCH];
+        for (int32_t u = 0; u < units; ++u) nk[u] = prefix_len - p.kv_lo;
+        pre = kca::make_rows_plan(units, nk, left, kca::kMultiRowMinSplit);
+        bytes = slots_bytes((size_t)batch * pre.max_splits * kHeads);
+        t = 17. + 1.1 * pre.split_len / kRowsStage;
+      }
+      kca::RowsPlan o = own_all;
+      if (c == 0) {
+        t += t_own;
+      } else {
+        o.split_len = (int32_t)(kca::cdiv(kca::cdiv(longest, c), kRowsStage) * kRowsStage);
+        o.max_splits = kca::rows_n_splits(longest, o.split_len);
+        const double t_beside = 2. + (double)o.split_len * 1024. / 50e3;
+        if (t_beside > t) t = t_beside;
+      }
+      t += 2e6 * (double)bytes / 6.5e12;
+      if (parts != 0 && t >= best) continue;
+      best = t;
+      parts = bytes;
+      p.tc = tc;
+      p.pre = pre;
+      p.unit_rows = ur;
+      p.own = o;
+      p.own_cluster = c == 0 ? own_all_cluster : c;
+    }
+  }
+  if (parts == 0 || (forced < 0 && t_joined <= best)) {
+    p.route = PrefixPlan::kJoined;
+    p.own = all;
+    p.own_cluster = joined_cluster;
+  } else {
+    p.own_parts += parts;
+  }
+  p.total = p.own_parts + mma_ws_bytes(p.own, p.own_cluster) - KCA_WORKSPACE_HEADER;
   *out = p;
   return KCA_OK;
 }
@@ -1186,7 +1269,7 @@ int attn_decode_blocks(const void* q, int32_t q_dtype, const void* k_cache, cons
   if (!mma) {
     a.part_slots = a.max_splits > 1 ? (int64_t)a.n_units * a.max_splits : 0;
     carve(workspace, (size_t)a.n_units * a.max_splits * kHeads * 2 * 4, &a.part_ml, &a.part_acc);
-    return kca::launch_rows_blocks(q_dtype, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+    return kca::launch_rows_src(kca::kSrcBlocks, q_dtype, a, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
   }
   a.cluster = cluster;
   a.max_clusters = (a.max_splits + cluster - 1) / cluster;
@@ -1209,12 +1292,14 @@ size_t attn_decode_prefix_workspace_bytes(int32_t q_dtype, int32_t kv_dtype, int
     return 0;
   for (int32_t b = 0; b < batch; ++b)
     if (ctx_len[b] < prefix_len || ctx_len[b] > KCA_MAX_POSITION) return 0;
-  // enough for the lengths themselves and for device lengths up to them
-  PrefixPlan a, b;
-  if (plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx_len, false, window, &a) != KCA_OK ||
-      plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx_len, true, window, &b) != KCA_OK)
+  // enough for the lengths themselves and for any up to the longest of them
+  PrefixPlan p;
+  int sms = 0;
+  if (current_sms(&sms) != KCA_OK ||
+      plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx_len, false, false, window, &p) != KCA_OK)
     return 0;
-  return a.total > b.total ? a.total : b.total;
+  const size_t bound = prefix_ws_bound(kv_dtype, batch, sms);
+  return p.total > bound ? p.total : bound;
 }
 
 int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, const void* prefix_v, int64_t prefix_len,
@@ -1243,25 +1328,14 @@ int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, con
     return KCA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0) return KCA_ERR_WORKSPACE;
   PrefixPlan p;
-  st = plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx, ctx_len_dev != nullptr, window, &p);
+  st = plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx, ctx_len_dev != nullptr, false, window, &p);
+  // a workspace sized for other lengths may hold only the plan of equal ones
+  if (st == KCA_OK && workspace_bytes < p.total)
+    st = plan_prefix(q_dtype, kv_dtype, prefix_len, batch, ctx, ctx_len_dev != nullptr, true, window, &p);
   if (st != KCA_OK) return st;
   if (workspace_bytes < p.total) return KCA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  float* own_rec = reinterpret_cast<float*>(ws + p.own_rec);
-  kca::PrefixMergeArgs m{};
-  m.own = own_rec;
-  m.out = out;
-  m.ctx_dev = ctx_len_dev;
-  m.status = reinterpret_cast<kca::DeviceStatus*>(ws);
-  m.ctx_min = prefix_len;
-  m.ctx_bound = ctx_bound;
-  m.group = 1;
-  m.batch = batch;
-  m.out_dtype = out_dtype;
-  m.mscale = 1.4426950408889634f;
-
-  kca::RowsArgs r{};   // the rows kernels' arguments, common to prefix and own keys
+  kca::RowsArgs r{};   // the decode kernel's arguments, and in part the units'
   r.q = q;
   r.status = workspace;
   r.n_units = batch;
@@ -1269,9 +1343,11 @@ int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, con
   r.scale = scale;
   r.ctx_dev = ctx_len_dev;
   r.ctx_bound = ctx_bound;
+  r.prefix_len = prefix_len;
   for (int32_t b = 0; b < batch; ++b) r.ctx[b] = ctx[b];
+  CUtensorMap tmpk, tmpv;   // the prefix
 
-  if (p.route == PrefixPlan::kTc) {
+  if (p.route == PrefixPlan::kTiles) {
     kca::TcPrefixArgs a{};
     a.plan = p.tc;
     a.q = q;
@@ -1279,11 +1355,11 @@ int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, con
     a.scale_log2 = scale * 1.4426950408889634f;
     a.ctx_dev = ctx_len_dev;
     for (int32_t b = 0; b < batch; ++b) a.first_key[b] = (int32_t)kca::lo_of(ctx[b] - 1, window);
-    carve(workspace, (size_t)p.tc.n_slots * 128 * 2 * 4, &a.part_ml, &a.part_acc, p.pre_parts);
+    carve(workspace, (size_t)p.tc.n_slots * 128 * 2 * 4, &a.part_ml, &a.part_acc);
     if (!kca::fill_tc_prefix_tables(a)) return KCA_ERR_RANGE;
-    CUtensorMap tmk, tmv, tmq, tmpart, tmpart_rag;
-    if (!encode_kv_map(&tmk, prefix_k, kv_dtype, p.kv_lo, prefix_len, 64) ||
-        !encode_kv_map(&tmv, prefix_v, kv_dtype, p.kv_lo, prefix_len, 64) ||
+    CUtensorMap tmq, tmpart, tmpart_rag;
+    if (!encode_kv_map(&tmpk, prefix_k, kv_dtype, p.kv_lo, prefix_len, 64) ||
+        !encode_kv_map(&tmpv, prefix_v, kv_dtype, p.kv_lo, prefix_len, 64) ||
         !encode_rows_map(&tmq, q, q_dtype, (int64_t)batch * kHeads, 64) ||
         !encode_rows_map(&tmpart, a.part_acc, KCA_F32, (int64_t)p.tc.n_slots * 128, 32))
       return KCA_ERR_CUDA;
@@ -1293,18 +1369,16 @@ int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, con
     if (rag != 0 && !encode_rows_map(&tmpart_rag, a.part_acc, KCA_F32, (int64_t)p.tc.n_slots * 128, 32,
                                      (uint32_t)(rag * kHeads)))
       return KCA_ERR_CUDA;
-    if (kca::launch_prefix_tc(kv_dtype, tmk, tmv, tmq, tmpart, tmpart_rag, a, s) != cudaSuccess) return KCA_ERR_CUDA;
-    m.ml = a.part_ml;
-    m.acc = a.part_acc;
-    m.group = kca::kRowTile;
-    m.group_step = (int64_t)p.tc.max_split * 128;
-    m.item_step = 128;
-    m.n_items = p.tc.max_split;
-    m.mscale = 1.f;
+    if (kca::launch_prefix_tc(kv_dtype, tmpk, tmpv, tmq, tmpart, tmpart_rag, a, s) != cudaSuccess) return KCA_ERR_CUDA;
+    r.pre_ml = a.part_ml;
+    r.pre_acc = a.part_acc;
+    r.pre_group = kca::kRowTile;
+    r.pre_group_step = (int64_t)p.tc.max_split * 128;
+    r.pre_item_step = 128;
+    r.pre_items = p.tc.max_split;
+    r.pre_mscale = 0.6931471805599453f;   // that kernel's reference maxima are in log2 units
   } else if (p.route == PrefixPlan::kUnits) {
     kca::RowsArgs a = r;
-    a.k = prefix_k;
-    a.v = prefix_v;
     a.mode = 3;
     a.rows_per_seq = batch;
     a.unit_rows = p.unit_rows;
@@ -1315,49 +1389,58 @@ int attn_decode_prefix(const void* q, int32_t q_dtype, const void* prefix_k, con
     a.key_end = prefix_len;
     a.cache_rows = prefix_len;
     a.part_slots = (int64_t)batch * a.max_splits;
-    carve(workspace, (size_t)a.part_slots * kHeads * 2 * 4, &a.part_ml, &a.part_acc, p.pre_parts);
-    CUtensorMap tmk, tmv;
-    if (!encode_kv_map(&tmk, prefix_k, kv_dtype, 0, prefix_len, 64) ||
-        !encode_kv_map(&tmv, prefix_v, kv_dtype, 0, prefix_len, 64) ||
-        kca::launch_rows_tc(q_dtype, kv_dtype, tmk, tmv, a, s) != cudaSuccess)
+    carve(workspace, (size_t)a.part_slots * kHeads * 2 * 4, &a.part_ml, &a.part_acc);
+    if (!encode_kv_map(&tmpk, prefix_k, kv_dtype, 0, prefix_len, 64) ||
+        !encode_kv_map(&tmpv, prefix_v, kv_dtype, 0, prefix_len, 64) ||
+        kca::launch_rows_tc(q_dtype, kv_dtype, tmpk, tmpv, a, s) != cudaSuccess)
       return KCA_ERR_CUDA;
-    m.ml = a.part_ml;
-    m.acc = a.part_acc;
-    m.group_step = (int64_t)a.max_splits * kHeads;
-    m.item_step = kHeads;
-    m.n_items = a.max_splits;
-  } else if (p.route == PrefixPlan::kRows) {
-    kca::RowsArgs a = r;
-    float* rec = reinterpret_cast<float*>(ws + p.pre_rec);
-    a.k = prefix_k;
-    a.v = prefix_v;
-    a.out_ml = rec;
-    a.out = rec + (size_t)batch * kHeads * 2;
-    a.seq_rows = 0;   // every sequence reads the same rows
-    a.key_end = prefix_len;
-    a.split_len = p.pre.split_len;
-    a.max_splits = p.pre.max_splits;
-    st = launch_rows_path(q_dtype, kv_dtype, prefix_k, prefix_v, prefix_len, a, p.pre_cluster, workspace, s,
-                          p.pre_parts);
-    if (st != KCA_OK) return st;
-    m.ml = a.out_ml;
-    m.acc = a.out;
-    m.group_step = kHeads;
-    m.n_items = 1;
+    r.pre_ml = a.part_ml;
+    r.pre_acc = a.part_acc;
+    r.pre_group = 1;
+    r.pre_group_step = (int64_t)a.max_splits * kHeads;
+    r.pre_item_step = kHeads;
+    r.pre_items = a.max_splits;
+    r.pre_mscale = 1.f;
   }
+
   r.k = k_cache;
   r.v = v_cache;
-  r.out_ml = own_rec;
-  r.out = own_rec + (size_t)batch * kHeads * 2;
+  r.out = static_cast<float*>(out);
+  r.out_dtype = out_dtype;
   r.seq_rows = capacity;
-  r.key_begin = prefix_len;
-  r.key_end = prefix_len + capacity;
   r.split_len = p.own.split_len;
   r.max_splits = p.own.max_splits;
-  st = launch_rows_path(q_dtype, kv_dtype, k_cache, v_cache, (int64_t)batch * capacity, r, p.own_cluster, workspace, s,
-                        p.own_parts);
-  if (st != KCA_OK) return st;
-  return kca::launch_prefix_merge(m, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+  r.cache_rows = (int64_t)batch * capacity;
+  if (p.own_cluster == 0) {   // f32 caches
+    r.prefix_k = prefix_k;
+    r.prefix_v = prefix_v;
+    r.part_slots = r.max_splits > 1 ? (int64_t)batch * r.max_splits : 0;
+    carve(workspace, (size_t)batch * r.max_splits * kHeads * 2 * 4, &r.part_ml, &r.part_acc);
+    return kca::launch_rows_src(kca::kSrcJoined, q_dtype, r, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
+  }
+  r.cluster = p.own_cluster;
+  r.max_clusters = (r.max_splits + r.cluster - 1) / r.cluster;
+  r.part_slots = r.max_clusters > 1 ? (int64_t)batch * r.max_clusters : 0;
+  if (r.max_clusters > 1) {
+    r.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kStatusBytes);
+    carve(workspace, (size_t)batch * r.max_clusters * kHeads * 2 * 4, &r.cpart_ml, &r.cpart_acc, p.own_parts);
+  }
+  CUtensorMap tmk, tmv;
+  if (!encode_kv_map(&tmk, k_cache, kv_dtype, 0, r.cache_rows, 64) ||
+      !encode_kv_map(&tmv, v_cache, kv_dtype, 0, r.cache_rows, 64))
+    return KCA_ERR_CUDA;
+  if (p.route == PrefixPlan::kJoined) {
+    tmpk = tmk;   // an empty prefix: never used
+    tmpv = tmv;
+    if (prefix_len > 0 && (!encode_kv_map(&tmpk, prefix_k, kv_dtype, 0, prefix_len, 64) ||
+                           !encode_kv_map(&tmpv, prefix_v, kv_dtype, 0, prefix_len, 64)))
+      return KCA_ERR_CUDA;
+    return kca::launch_decode_mma_joined(q_dtype, kv_dtype, tmk, tmv, tmpk, tmpv, r, s) == cudaSuccess ? KCA_OK
+                                                                                                       : KCA_ERR_CUDA;
+  }
+  r.key_begin = prefix_len;
+  r.key_end = prefix_len + capacity;
+  return kca::launch_decode_mma_own(q_dtype, kv_dtype, tmk, tmv, r, s) == cudaSuccess ? KCA_OK : KCA_ERR_CUDA;
 }
 
 int attn_merge_partials(int32_t n_parts, int32_t batch, const float* parts, int64_t part_stride, float* out,

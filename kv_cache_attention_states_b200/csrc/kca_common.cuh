@@ -181,6 +181,20 @@ __device__ __forceinline__ void load8<KCA_BF16>(const void* p, float (&x)[8]) {
   }
 }
 
+// The same past L1.
+template <int DT>
+__device__ __forceinline__ void load8_l2(const void* p, float (&x)[8]) {
+  if (DT == KCA_F32) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+    return;
+  }
+  const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p));
+  load8<DT>(&u, x);
+}
+
 template <int DT>
 struct ElemBytes { static constexpr int value = (DT == KCA_F32) ? 4 : 2; };
 

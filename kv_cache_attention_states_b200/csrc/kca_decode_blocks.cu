@@ -1,0 +1,21 @@
+// kca_decode_blocks.cu -- the decode kernel (kca_decode_mma.cuh) over listed
+// blocks of keys (attn_decode_blocks).
+#include "kca_decode_mma.cuh"
+
+namespace kca {
+
+cudaError_t launch_decode_mma_blocks(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                     const RowsArgs& a, cudaStream_t stream) {
+#define KCA_DBLK_CASE(QD, KD) \
+  if (q_dtype == QD && kv_dtype == KD) return launch_t<QD, KD, KD, kSrcBlocks>({tmk, tmv, tmk}, a, stream);
+  KCA_DBLK_CASE(KCA_F32, KCA_F16)
+  KCA_DBLK_CASE(KCA_F32, KCA_BF16)
+  KCA_DBLK_CASE(KCA_F16, KCA_F16)
+  KCA_DBLK_CASE(KCA_F16, KCA_BF16)
+  KCA_DBLK_CASE(KCA_BF16, KCA_F16)
+  KCA_DBLK_CASE(KCA_BF16, KCA_BF16)
+#undef KCA_DBLK_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kca

@@ -1,0 +1,37 @@
+// kca_decode_prefix.cu -- the decode kernel (kca_decode_mma.cuh) of a batch over
+// a shared prefix (attn_decode_prefix): every sequence over prefix and own keys
+// (joined), or over its own keys with the prefix's partials merged in.
+#include "kca_decode_mma.cuh"
+
+namespace kca {
+
+cudaError_t launch_decode_mma_joined(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                     const CUtensorMap& tmpk, const CUtensorMap& tmpv, const RowsArgs& a,
+                                     cudaStream_t stream) {
+#define KCA_DJOIN_CASE(QD, KD) \
+  if (q_dtype == QD && kv_dtype == KD) return launch_t<QD, KD, KD, kSrcJoined>({tmk, tmv, tmk, tmpk, tmpv}, a, stream);
+  KCA_DJOIN_CASE(KCA_F32, KCA_F16)
+  KCA_DJOIN_CASE(KCA_F32, KCA_BF16)
+  KCA_DJOIN_CASE(KCA_F16, KCA_F16)
+  KCA_DJOIN_CASE(KCA_F16, KCA_BF16)
+  KCA_DJOIN_CASE(KCA_BF16, KCA_F16)
+  KCA_DJOIN_CASE(KCA_BF16, KCA_BF16)
+#undef KCA_DJOIN_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_mma_own(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                  const RowsArgs& a, cudaStream_t stream) {
+#define KCA_DOWN_CASE(QD, KD) \
+  if (q_dtype == QD && kv_dtype == KD) return launch_t<QD, KD, KD, kSrcOwn>({tmk, tmv, tmk}, a, stream);
+  KCA_DOWN_CASE(KCA_F32, KCA_F16)
+  KCA_DOWN_CASE(KCA_F32, KCA_BF16)
+  KCA_DOWN_CASE(KCA_F16, KCA_F16)
+  KCA_DOWN_CASE(KCA_F16, KCA_BF16)
+  KCA_DOWN_CASE(KCA_BF16, KCA_F16)
+  KCA_DOWN_CASE(KCA_BF16, KCA_BF16)
+#undef KCA_DOWN_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kca

@@ -126,7 +126,9 @@ inline RowsPlan make_cluster_rows_plan(int32_t n_units, const int64_t* nkeys, in
   };
   int64_t hi = cdiv(max_keys > kRowsMmaStage ? max_keys : kRowsMmaStage, kRowsMmaStage);
   int64_t lo = 1;
-  if (count(lo * kRowsMmaStage) <= target) {
+  if (n_units > target) {
+    // no length fits: one split a unit
+  } else if (count(lo * kRowsMmaStage) <= target) {
     hi = lo;
   } else {
     while (lo + 1 < hi) {
@@ -251,8 +253,7 @@ inline TcPlan make_tc_prefix_plan(int64_t kv_lo, int64_t prefix_len, int32_t row
   p.n_tiles = (int32_t)cdiv(rows, kRowTile);
   p.n_pairs = (int32_t)cdiv(p.n_tiles, 2);
   const int32_t n = (int32_t)cdiv(prefix_len - kv_lo, kKeyTile);
-  const int32_t budget = pair_budget > 80 ? 80 : pair_budget;   // the launch's item table
-  int32_t s = budget / p.n_pairs;
+  int32_t s = (pair_budget > 80 ? 80 : pair_budget) / p.n_pairs;   // 80: the launch's item table
   if (s < 1) s = 1;
   p.per_item = (int32_t)cdiv(n, s);
   if (p.per_item < kTcMinItemTiles) p.per_item = kTcMinItemTiles;

@@ -92,13 +92,14 @@ __device__ __forceinline__ uint32_t q8_code(float x, float sx) {
   return static_cast<uint32_t>(c) & 0xffu;
 }
 
-// BLK: attention over listed blocks of 64 keys (kca_rows.h): "key" p of a
-// split is key p % 64 of list entry p / 64, so a stage of 16 keys stays inside
-// one block.
-template <int QT, int KT, int VT = KT, bool DP4A = true, bool BLK = false>
+// SRC (RowsSrc, kca_rows.h): with listed blocks, "key" p of a split is key
+// p % 64 of list entry p / 64; with a shared prefix, number p of JoinedKeys.
+// Either way a stage of 16 keys stays inside one block or part.
+template <int QT, int KT, int VT = KT, bool DP4A = true, int SRC = kSrcRange>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a) {
   using S = RowsSmem<KT, VT>;
   constexpr bool kQ8 = KT == KCA_I8;
+  constexpr bool kBlk = SRC == kSrcBlocks, kJoin = SRC == kSrcJoined;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOffset);
   uint64_t* empty = full + kStages;
@@ -112,14 +113,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
 
   int64_t seq_base = (int64_t)unit * a.seq_rows;
   int64_t lo = 0, ctx = 0, nkeys;
-  if constexpr (BLK) {
+  JoinedKeys jk{};
+  if constexpr (kBlk) {
     ctx = rows_ctx(a, unit, split == 0 && threadIdx.x == 0);
     nkeys = (int64_t)a.n_list * KCA_BLOCK_KEYS;
+  } else if constexpr (kJoin) {
+    jk = joined_keys(a, unit, split == 0 && threadIdx.x == 0);
+    nkeys = jk.virtual_keys();
   } else {
     const int64_t pos = rows_unit_pos(a, unit, split == 0 && threadIdx.x == 0, &seq_base);
     nkeys = rows_keys(a, pos, &lo);
   }
-  const int32_t split_len = BLK ? a.split_len : rows_split_len(a, nkeys, kRowsSplitQuantum);
+  const int32_t split_len = kBlk ? a.split_len : rows_split_len(a, nkeys, kRowsSplitQuantum);
   const int32_t nsplit = rows_n_splits(nkeys, split_len);
   if (split >= nsplit) return;
   const int64_t kbeg = lo + (int64_t)split * split_len;
@@ -131,31 +136,36 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
   // bounds-checked builds: the split's rows lie in the cache and its partial
   // slot in the workspace (no CTA of this kernel waits on another)
   if (!KCA_IN_BOUNDS(nsplit <= a.max_splits &&
-                         (BLK ? seq_base + a.seq_rows <= a.cache_rows
-                              : base_row + kbeg >= 0 && base_row + kend <= a.cache_rows) &&
+                         (kBlk || kJoin ? seq_base + a.seq_rows <= a.cache_rows
+                                        : base_row + kbeg >= 0 && base_row + kend <= a.cache_rows) &&
                          (nsplit == 1 || (int64_t)(unit + 1) * a.max_splits <= a.part_slots),
                      status, kSiteBoundsRows, (unsigned)unit))
     return;
 
   if (nkeys == 0) {  // fully masked row: exactly zero (as a partial: (-inf, 0, 0))
     if (warp < kComputeWarps)
-      for (int i = threadIdx.x; i < kHeads * kDim; i += kComputeWarps * 32) out[i] = 0.f;
+      for (int i = threadIdx.x; i < kHeads * kDim; i += kComputeWarps * 32)
+        rows_store<SRC>(a, (int64_t)unit * kHeads * kDim + i, 0.f);
     if (threadIdx.x < kHeads) rows_write_ml(a, unit, threadIdx.x, -INFINITY, 0.f);
     return;
   }
   const int n_stage = (int)cdiv(kend - kbeg, kKeysPerStage);
-  // Keys of stage i, the first at cache row *row.
-  auto stage_keys = [&](int i, int64_t* row) -> int {
+  // Keys of stage i, the first at row *row of the cache or (*prefix) the prefix.
+  auto stage_keys = [&](int i, int64_t* row, bool* prefix) -> int {
     const int64_t k0 = kbeg + (int64_t)i * kKeysPerStage;
     int64_t left = kend - k0;
     *row = base_row + k0;
-    if constexpr (BLK) {
+    *prefix = false;
+    if constexpr (kBlk) {
       const int64_t id = rows_block(a, unit, (int)(k0 / KCA_BLOCK_KEYS), ctx);
       const int64_t p = id * KCA_BLOCK_KEYS + k0 % KCA_BLOCK_KEYS;   // position of the stage's first key
-      left = id < 0 || p >= ctx ? 0 : ctx - p;
+      left = id < 0 ? 0 : ctx - p;
       *row = seq_base + p;
+    } else if constexpr (kJoin) {
+      left = jk.stage(k0, row, prefix);
+      if (!*prefix) *row += seq_base;
     }
-    return (int)(left < kKeysPerStage ? left : kKeysPerStage);
+    return (int)(left < 0 ? 0 : left < kKeysPerStage ? left : kKeysPerStage);
   };
 
   if (threadIdx.x == 0) {
@@ -181,8 +191,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
             !mbar_wait(&empty[slot], ((i / kStages) - 1) & 1, abort_flag, status, kSiteRowsEmpty))
           break;
         int64_t row0;
-        const int cnt = stage_keys(i, &row0);
-        if (BLK && cnt == 0) {   // no block, or past the context: an empty stage
+        bool prefix;
+        const int cnt = stage_keys(i, &row0, &prefix);
+        if (SRC != kSrcRange && cnt == 0) {   // no block, or past the keys: an empty stage
           mbar_arrive(&full[slot]);
           issued = i + 1;
           continue;
@@ -191,8 +202,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
         const uint32_t vbytes = (uint32_t)cnt * S::kVRowBytes;
         unsigned char* dst = smem + slot * S::kStageBytes;
         mbar_arrive_expect_tx(&full[slot], kbytes + vbytes);
-        bulk_g2s(dst, kg + row0 * S::kKRowBytes, kbytes, &full[slot]);
-        bulk_g2s(dst + kKeysPerStage * S::kKRowBytes, vg + row0 * S::kVRowBytes, vbytes,
+        const char* ks = kJoin && prefix ? static_cast<const char*>(a.prefix_k) : kg;
+        const char* vs = kJoin && prefix ? static_cast<const char*>(a.prefix_v) : vg;
+        bulk_g2s(dst, ks + row0 * S::kKRowBytes, kbytes, &full[slot]);
+        bulk_g2s(dst + kKeysPerStage * S::kKRowBytes, vs + row0 * S::kVRowBytes, vbytes,
                  &full[slot]);
         issued = i + 1;
       }
@@ -255,7 +268,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
                       mbar_wait(&full[slot], (i / kStages) & 1, abort_flag, status, kSiteRowsFull));
       if (!ok) break;
       int64_t row0;
-      const int cnt = stage_keys(i, &row0);
+      bool prefix;
+      const int cnt = stage_keys(i, &row0, &prefix);
       const unsigned char* st = smem + slot * S::kStageBytes;
       const int nk = (warp < cnt ? 1 : 0) + (warp + kComputeWarps < cnt ? 1 : 0);
       if (nk > 0) {
@@ -370,10 +384,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
         A[0] += f * x0.x; A[1] += f * x0.y; A[2] += f * x0.z; A[3] += f * x0.w;
         A[4] += f * x1.x; A[5] += f * x1.y; A[6] += f * x1.z; A[7] += f * x1.w;
       }
-      if (BLK && nsplit == 1) {
+      if (SRC != kSrcRange && nsplit == 1) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-          rows_store<BLK>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, rows_final(a, A[t], M, L));
+          rows_store<SRC>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, rows_final(a, A[t], M, L));
       } else if (nsplit == 1) {
         const float inv = a.out_ml != nullptr ? 1.f : 1.f / L;
         float4* o = reinterpret_cast<float4*>(out + h * kDim + 8 * lane);
@@ -395,13 +409,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const RowsArgs a)
 }
 
 // Log-sum-exp merge of the splits of each unit: one CTA per (unit, head),
-// its eight warps taking interleaved splits.  BLK: the block variant's splits
-// and output type (the merged row passes through shared memory).
-template <bool BLK>
+// its eight warps taking interleaved splits.  SRC: as in rows_kernel; other
+// than a range, the merged row passes through shared memory to its type.
+template <int SRC>
 __global__ void __launch_bounds__(256) merge_rows_kernel(const RowsArgs a) {
   const int unit = blockIdx.x >> 3, h = blockIdx.x & 7;
-  if constexpr (BLK) {
-    const int32_t ns = rows_n_splits((int64_t)a.n_list * KCA_BLOCK_KEYS, a.split_len);
+  if constexpr (SRC != kSrcRange) {
+    int64_t nkeys = (int64_t)a.n_list * KCA_BLOCK_KEYS;
+    int32_t split_len = a.split_len;
+    if (SRC == kSrcJoined) {
+      nkeys = joined_keys(a, unit, false).virtual_keys();
+      split_len = rows_split_len(a, nkeys, kRowsSplitQuantum);
+    }
+    const int32_t ns = rows_n_splits(nkeys, split_len);
+    if (ns <= 1) return;   // that split wrote the output
     if (!KCA_IN_BOUNDS(ns <= a.max_splits && (int64_t)(unit + 1) * a.max_splits <= a.part_slots,
                        static_cast<DeviceStatus*>(a.status), kSiteBoundsMerge, (unsigned)unit))
       return;
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const RowsArgs a) {
                  threadIdx.x >> 5, lane, 1);
     if (threadIdx.x < 32)   // the group's first warp wrote the row, each lane its own dims
       for (int t = 0; t < 8; ++t)
-        rows_store<BLK>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, row[8 * lane + t]);
+        rows_store<SRC>(a, ((int64_t)unit * kHeads + h) * kDim + 8 * lane + t, row[8 * lane + t]);
     return;
   }
   int64_t seq_base;
@@ -432,10 +453,10 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const RowsArgs a) {
                threadIdx.x & 31, 1, a.out_ml != nullptr ? a.out_ml + ((int64_t)unit * kHeads + h) * 2 : nullptr);
 }
 
-template <int QT, int KT, int VT = KT, bool DP4A = true, bool BLK = false>
+template <int QT, int KT, int VT = KT, bool DP4A = true, int SRC = kSrcRange>
 cudaError_t launch_rows_t(const RowsArgs& a, cudaStream_t stream) {
   using S = RowsSmem<KT, VT>;
-  auto kern = rows_kernel<QT, KT, VT, DP4A, BLK>;
+  auto kern = rows_kernel<QT, KT, VT, DP4A, SRC>;
   static std::atomic<bool> attr_set[64];   // per device; zero-initialised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -449,22 +470,28 @@ cudaError_t launch_rows_t(const RowsArgs& a, cudaStream_t stream) {
   kern<<<grid, kRowsThreads, S::kTotal, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.max_splits <= 1) return e;
-  if (!BLK) return launch_merge_rows(a, stream);
-  merge_rows_kernel<true><<<a.n_units * kHeads, 256, 0, stream>>>(a);
+  if (SRC == kSrcRange) return launch_merge_rows(a, stream);
+  merge_rows_kernel<SRC><<<a.n_units * kHeads, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_merge_rows(const RowsArgs& a, cudaStream_t stream) {
-  merge_rows_kernel<false><<<a.n_units * kHeads, 256, 0, stream>>>(a);
+  merge_rows_kernel<kSrcRange><<<a.n_units * kHeads, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_rows_blocks(int q_dtype, const RowsArgs& a, cudaStream_t stream) {
-  if (q_dtype == KCA_F32) return launch_rows_t<KCA_F32, KCA_F32, KCA_F32, true, true>(a, stream);
-  if (q_dtype == KCA_F16) return launch_rows_t<KCA_F16, KCA_F32, KCA_F32, true, true>(a, stream);
-  if (q_dtype == KCA_BF16) return launch_rows_t<KCA_BF16, KCA_F32, KCA_F32, true, true>(a, stream);
+cudaError_t launch_rows_src(int src, int q_dtype, const RowsArgs& a, cudaStream_t stream) {
+#define KCA_SRC_CASE(SRC, QD) \
+  if (src == SRC && q_dtype == QD) return launch_rows_t<QD, KCA_F32, KCA_F32, true, SRC>(a, stream);
+  KCA_SRC_CASE(kSrcBlocks, KCA_F32)
+  KCA_SRC_CASE(kSrcBlocks, KCA_F16)
+  KCA_SRC_CASE(kSrcBlocks, KCA_BF16)
+  KCA_SRC_CASE(kSrcJoined, KCA_F32)
+  KCA_SRC_CASE(kSrcJoined, KCA_F16)
+  KCA_SRC_CASE(kSrcJoined, KCA_BF16)
+#undef KCA_SRC_CASE
   return cudaErrorInvalidValue;
 }
 

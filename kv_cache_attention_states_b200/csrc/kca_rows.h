@@ -8,7 +8,12 @@
 
 namespace kca {
 
-struct DeviceStatus;
+// Where the keys of a decode kernel's units lie (a template argument of the
+// kernels): a range of the unit's cache, listed blocks of it, a shared prefix
+// followed by the unit's own keys, or its own keys with the partials of a
+// prefix merged in (16-bit caches).  out is f32, or of out_dtype except for a
+// range.
+enum RowsSrc { kSrcRange, kSrcBlocks, kSrcJoined, kSrcOwn };
 
 struct RowsArgs {
   const void* q;         // [n_units][8][256]
@@ -60,13 +65,29 @@ struct RowsArgs {
   int64_t cache_rows;
   int64_t part_slots;
   int64_t ctx[KCA_MAX_BATCH];  // decode: ctx_len per sequence
-  // Block lists (the kernels' block variants; attn_decode_blocks): unit u
+  // Block lists (kSrcBlocks; attn_decode_blocks): unit u
   // attends to the blocks of 64 keys at blocks[u * n_list ..] (-1: none)
   // instead of a key range, "key" p of its splits being key p % 64 of list
   // entry p / 64; out is of out_dtype.
   const int32_t* blocks;
   int32_t n_list;
   int32_t out_dtype;
+  // Shared prefix: positions 0 .. prefix_len - 1 (f32 caches: their rows here;
+  // 16-bit ones through tensor maps); cache row r of a sequence holds position
+  // prefix_len + r.
+  int64_t prefix_len;
+  const void* prefix_k;
+  const void* prefix_v;
+  // Its partials (kSrcOwn): partial s of (unit u, head h) at index
+  // (u / pre_group) * pre_group_step + s * pre_item_step + (u % pre_group) * 8 + h
+  // of pre_ml (m, l) and pre_acc [256]; m * pre_mscale is in natural units.
+  const float* pre_ml;
+  const float* pre_acc;
+  int64_t pre_group_step;
+  int64_t pre_item_step;
+  int32_t pre_group;
+  int32_t pre_items;
+  float pre_mscale;
 };
 
 // Rows of one unit of the batched multi-row kernels: 4 (both kernels), or 8
@@ -83,7 +104,7 @@ namespace kca {
 // empty context, so no row past the bound is ever touched.
 __device__ __forceinline__ int64_t rows_ctx(const RowsArgs& a, int unit, bool record) {
   if (a.ctx_dev == nullptr) return a.ctx[unit];
-  const int64_t c = a.ctx_dev[unit];
+  const int64_t c = __ldcg(a.ctx_dev + unit);
   if (c >= 0 && c <= a.ctx_bound) return c;
   if (record) record_error(static_cast<DeviceStatus*>(a.status), kSiteCtx, kErrBadCtx, (unsigned)unit);
   return 0;
@@ -121,7 +142,46 @@ __device__ __forceinline__ float rows_final(const RowsArgs& a, float acc, float 
   if (a.out_ml != nullptr) return acc;
   return (M == -INFINITY && L == 0.f) ? 0.f : acc / L;
 }
-// Block variants: entry i of unit's list as a block index whose first key the
+// kSrcOwn: whether ctx is the length of a sequence that has the prefix; a
+// shorter one is recorded.
+__device__ __forceinline__ bool rows_past_prefix(const RowsArgs& a, int unit, int64_t ctx, bool record) {
+  const bool ok = ctx >= a.prefix_len;
+  if (!ok && record) record_error(static_cast<DeviceStatus*>(a.status), kSiteCtx, kErrBadCtx, (unsigned)unit);
+  return ok;
+}
+// kSrcJoined: the keys of a unit in one numbering, the n_p visible prefix keys
+// (from position lo_p on) padded to whole stages of 64, then the n_o own ones
+// (from lo_o on).  A length that is not one of a sequence with this prefix is
+// recorded (when `record`) and sees nothing.
+constexpr int kJoinedStage = 64;
+struct JoinedKeys {
+  int64_t lo_p, n_p, lo_o, n_o, own_row;   // own_row: the cache row of position lo_o within its sequence
+  __device__ __forceinline__ int64_t prefix_keys() const { return (n_p + kJoinedStage - 1) / kJoinedStage * kJoinedStage; }
+  __device__ __forceinline__ int64_t virtual_keys() const {
+    return prefix_keys() + (n_o + kJoinedStage - 1) / kJoinedStage * kJoinedStage;
+  }
+  // Keys from number p on to the end of its part (0 or less: padding), the
+  // first at row *row of the prefix (*prefix) or of the sequence.
+  __device__ __forceinline__ int64_t stage(int64_t p, int64_t* row, bool* prefix) const {
+    const int64_t in_p = prefix_keys();
+    *prefix = p < in_p;
+    *row = p < in_p ? lo_p + p : own_row + (p - in_p);
+    return p < in_p ? n_p - p : n_o - (p - in_p);
+  }
+};
+__device__ __forceinline__ JoinedKeys joined_keys(const RowsArgs& a, int unit, bool record) {
+  JoinedKeys j{};
+  const int64_t ctx = rows_ctx(a, unit, record);
+  if (!rows_past_prefix(a, unit, ctx, record)) return j;
+  const int64_t lo = lo_of(ctx - 1, a.window);
+  j.lo_p = lo < a.prefix_len ? lo : a.prefix_len;
+  j.n_p = a.prefix_len - j.lo_p;
+  j.lo_o = lo < a.prefix_len ? a.prefix_len : lo;
+  j.n_o = ctx - j.lo_o;
+  j.own_row = j.lo_o - a.prefix_len;
+  return j;
+}
+// kSrcBlocks: entry i of unit's list as a block index whose first key the
 // sequence has (ctx: its length), or -1; anything else listed is recorded.
 __device__ __forceinline__ int rows_block(const RowsArgs& a, int unit, int i, int64_t ctx) {
   const int32_t id = a.blocks[(int64_t)unit * a.n_list + i];
@@ -129,12 +189,12 @@ __device__ __forceinline__ int rows_block(const RowsArgs& a, int unit, int i, in
   if (id != -1) record_error(static_cast<DeviceStatus*>(a.status), kSiteBlock, kErrBadBlock, (unsigned)unit);
   return -1;
 }
-// One output value at element idx of out: f32, or with the block variants of
-// out_dtype (rounded once, to nearest even).
-template <bool BLK>
+// One output value at element idx of out: f32, or of out_dtype (rounded once,
+// to nearest even).
+template <int SRC>
 __device__ __forceinline__ void rows_store(const RowsArgs& a, int64_t idx, float v) {
-  if (BLK && a.out_dtype == KCA_F16) reinterpret_cast<__half*>(a.out)[idx] = __float2half_rn(v);
-  else if (BLK && a.out_dtype == KCA_BF16) reinterpret_cast<__nv_bfloat16*>(a.out)[idx] = __float2bfloat16_rn(v);
+  if (SRC != kSrcRange && a.out_dtype == KCA_F16) reinterpret_cast<__half*>(a.out)[idx] = __float2half_rn(v);
+  else if (SRC != kSrcRange && a.out_dtype == KCA_BF16) reinterpret_cast<__nv_bfloat16*>(a.out)[idx] = __float2bfloat16_rn(v);
   else a.out[idx] = v;
 }
 // Unit u of a batched call in multi-row units (a.unit_rows rows each):
@@ -162,8 +222,9 @@ __device__ __forceinline__ void multirow_unit(const RowsArgs& a, int u, int* b, 
 
 cudaError_t launch_rows(int q_dtype, int kv_dtype, const RowsArgs& a, cudaStream_t stream);
 
-// The block variant for f32 caches (a.blocks set; a.ctx_dev gives the lengths).
-cudaError_t launch_rows_blocks(int q_dtype, const RowsArgs& a, cudaStream_t stream);
+// f32 caches over listed blocks (a.blocks set; a.ctx_dev gives the lengths) or
+// over a shared prefix and own keys (a.prefix_k, a.prefix_v).
+cudaError_t launch_rows_src(int src, int q_dtype, const RowsArgs& a, cudaStream_t stream);
 
 // The CUDA-core rows kernel with packed int8 K rows (KCA_I8) and V of
 // v_dtype: the quantised-dot variant; dp4a selects the instruction over its
@@ -225,24 +286,6 @@ cudaError_t launch_rows_tc(int q_dtype, int kv_dtype, const CUtensorMap& tmk, co
 constexpr int kRowsTcMergeSplits = 16;
 cudaError_t launch_multirow_merge(const RowsArgs& a, cudaStream_t stream);
 
-// Merge of attn_decode_prefix (kca_prefix.cu): row (b, h) of the output is the
-// log-sum-exp combination of n_items partials of the prefix -- item s at index
-// (b / group) * group_step + s * item_step + (b % group) * 8 + h of ml / acc --
-// and the record of the sequence's own keys (layout of attn_decode_partial).
-struct PrefixMergeArgs {
-  const float* ml;
-  const float* acc;
-  const float* own;
-  void* out;
-  const int64_t* ctx_dev;   // lengths outside ctx_min..ctx_bound: zeros, recorded
-  DeviceStatus* status;
-  int64_t ctx_min, ctx_bound;
-  int64_t group_step, item_step;
-  int32_t group, n_items, batch, out_dtype;
-  float mscale;             // the items' m to log2 units
-};
-cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, cudaStream_t stream);
-
 // Clusters of c CTAs of the tensor-core rows kernel that fit on the device at
 // once (0 on failure).
 int decode_mma_cluster_capacity(int c);
@@ -255,5 +298,13 @@ cudaError_t launch_decode_mma(int q_dtype, int kv_dtype, const CUtensorMap& tmk,
 // The same over listed blocks (a.blocks set; a.ctx_dev gives the lengths).
 cudaError_t launch_decode_mma_blocks(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                      const RowsArgs& a, cudaStream_t stream);
+// The same over a shared prefix (maps tmpk / tmpv) and own keys, and over own
+// keys with the prefix's partials merged in: to be launched right behind the
+// kernel that writes them.
+cudaError_t launch_decode_mma_joined(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                     const CUtensorMap& tmpk, const CUtensorMap& tmpv, const RowsArgs& a,
+                                     cudaStream_t stream);
+cudaError_t launch_decode_mma_own(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                  const RowsArgs& a, cudaStream_t stream);
 
 }  // namespace kca

@@ -211,6 +211,9 @@ __global__ void __launch_bounds__(RowsTc<UR>::kThreads, 1)
   // Programmatic dependent launch: the set-up above overlaps the previous
   // kernel of the stream; global memory is touched only after this wait.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Over a shared prefix the kernel behind this one has its own keys to stream
+  // before it needs the partials.
+  if (shared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Stage the queries: M row m = 32 q + 16 part + 8 (i % 2) + h for query
   // row i = 2 q + ..., head h, part 0 (high) or 1 (low); absent rows zero.

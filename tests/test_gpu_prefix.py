@@ -20,6 +20,12 @@ def _setup(cuda_ok):
     kca.lib()
 
 
+@pytest.fixture(autouse=True)
+def _unpinned():
+    yield
+    kca.attn_force_path(kca.OP_PREFILL, kca.PATH_AUTO)
+
+
 def _i64(x):
     return torch.tensor(np.asarray(x, dtype=np.int64), device="cuda")
 
@@ -33,7 +39,7 @@ def _data(seed, batch, prefix, cap, qd, kv):
 def _check(got, od, data, qd, kv, ctx, window, seqs=None):
     q, pk, pv, k, v = data
     got = got.float().cpu().numpy().astype(np.float64)
-    tc = qd == kv and kv != "f32" and len(ctx) >= 3
+    tc = qd == kv and kv != "f32"   # may take the tiles, which round the probabilities
     for b in seqs if seqs is not None else range(len(ctx)):
         want, absqk, vmax, pabsv, n = op.attend(q[b], qd, pk, pv, k[b], v[b], kv, ctx[b], window)
         base = rounded_probabilities(kv, absqk, vmax, pabsv, n) if tc else f32_grade(qd, kv, absqk, vmax)[:, None]
@@ -53,6 +59,14 @@ def _run(data, qd, kv, ctx, window=0, od="f32", device=False, ws=None, out=None,
     return got
 
 
+# the forms that a call may take (16-bit caches): pinned, and as the library chooses
+FORMS = {"auto": kca.PATH_AUTO, "joined": kca.PATH_ROWS, "tiles": kca.PATH_TENSOR_CORE, "units": kca.PATH_MULTI_ROW}
+
+
+def _form(name):
+    return kca.forced_path(kca.OP_PREFILL, FORMS[name])
+
+
 PAIRS = [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("f32", "f16", "f32"), ("f32", "bf16", "f32"),
          ("f32", "f32", "f32"), ("f16", "bf16", "f16"), ("bf16", "f32", "bf16")]
 
@@ -61,28 +75,35 @@ PAIRS = [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("f32", "f16", "f32"),
 @pytest.mark.parametrize("batch,prefix,cap", [(1, 300, 70), (2, 1, 64), (3, 1000, 77), (5, 129, 1), (9, 2600, 300),
                                               (17, 700, 33), (33, 260, 20)])
 @pytest.mark.parametrize("device", [False, True])
-def test_matches_oracle(qd, kv, od, batch, prefix, cap, device):
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+def test_matches_oracle(qd, kv, od, batch, prefix, cap, device, form):
     data = _data(40, batch, prefix, cap, qd, kv)
     ctx = [prefix + int(c) for c in synth.integers(41, "c", 0, cap, batch)]
     ctx[0], ctx[-1] = prefix + cap, prefix
-    _check(_run(data, qd, kv, ctx, od=od, device=device), od, data, qd, kv, ctx, 0)
+    with _form(form):
+        got = _run(data, qd, kv, ctx, od=od, device=device)
+    _check(got, od, data, qd, kv, ctx, 0)
 
 
 @pytest.mark.parametrize("qd,kv,od", PAIRS)
 @pytest.mark.parametrize("batch,prefix,cap,window", [(4, 900, 400, 300), (20, 900, 40, 333), (3, 128, 200, 1),
                                                      (2, 500, 100, 64), (1, 1000, 30, 500), (40, 700, 90, 5000)])
 @pytest.mark.parametrize("device", [False, True])
-def test_windows_cut_the_prefix(qd, kv, od, batch, prefix, cap, window, device):
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+def test_windows_cut_the_prefix(qd, kv, od, batch, prefix, cap, window, device, form):
     data = _data(42, batch, prefix, cap, qd, kv)
     ctx = [prefix + int(c) for c in synth.integers(43, "c", 0, cap, batch)]
     ctx[0] = prefix + cap
-    _check(_run(data, qd, kv, ctx, window, od, device), od, data, qd, kv, ctx, window)
+    with _form(form):
+        got = _run(data, qd, kv, ctx, window, od, device)
+    _check(got, od, data, qd, kv, ctx, window)
 
 
 @pytest.mark.parametrize("qd,kv", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
 @pytest.mark.parametrize("window", [0, 200])
 @pytest.mark.parametrize("device", [False, True])
-def test_border_keys(qd, kv, window, device):
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+def test_border_keys(qd, kv, window, device, form):
     """One key of each sequence draws nearly all of its weight when it is seen;
     the keys chosen lie on each side of every border."""
     prefix, cap = 385, 70
@@ -102,7 +123,8 @@ def test_border_keys(qd, kv, window, device):
             (pk1 if p < prefix else k1[b])[p if p < prefix else p - prefix] = one     # score 16 against N(0, 1)
             (pv1 if p < prefix else v1[b])[p if p < prefix else p - prefix] = three
             d = (q1, pk1, pv1, k1, v1)
-            got = _run(d, qd, kv, ctx, window, device=device)
+            with _form(form):
+                got = _run(d, qd, kv, ctx, window, device=device)
             _check(got, "f32", d, qd, kv, ctx, window, seqs=[b])
             assert bool((got[b] > 2.5).all()) == (first <= p < ctx[b]), (b, p)
 
@@ -125,7 +147,8 @@ def test_no_key_and_no_prefix(qd, kv):
 
 @pytest.mark.parametrize("qd,kv", [("f16", "f16"), ("f32", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("window", [0, 150])
-def test_rows_that_no_query_sees_may_hold_anything(qd, kv, window):
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+def test_rows_that_no_query_sees_may_hold_anything(qd, kv, window, form):
     prefix, cap, batch = 333, 50, 5
     data = _data(46, batch, prefix, cap, qd, kv)
     ctx = [prefix + c for c in (50, 0, 1, 30, 49)]
@@ -136,13 +159,16 @@ def test_rows_that_no_query_sees_may_hold_anything(qd, kv, window):
     pk[prefix:], pv[prefix:] = float("nan"), float("nan")        # a longer buffer than the prefix
     if window:
         pk[:prefix - window], pv[:prefix - window] = float("inf"), float("nan")
-    got = kca.attn_decode_prefix(q, pk, pv, prefix, k, v, ctx, window)
+    with _form(form):
+        got = kca.attn_decode_prefix(q, pk, pv, prefix, k, v, ctx, window)
     _check(got, "f32", data, qd, kv, ctx, window)
 
 
-def test_bad_device_lengths_give_zeros_and_are_recorded():
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+@pytest.mark.parametrize("qd,kv", [("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
+def test_bad_device_lengths_give_zeros_and_are_recorded(qd, kv, form):
     prefix, cap, batch = 500, 60, 6
-    for qd, kv in (("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")):
+    with _form(form):
         data = _data(47, batch, prefix, cap, qd, kv)
         ctx = [540, 499, 561, -1, 560, 1 << 40]
         ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(
@@ -182,7 +208,8 @@ def test_large_scores_in_one_sequence_only():
 
 @pytest.mark.parametrize("qd,kv,batch", [("bf16", "bf16", 4), ("f32", "f16", 3), ("f32", "f32", 2)])
 @pytest.mark.parametrize("window", [0, 400])
-def test_captured_step_follows_device_lengths(qd, kv, batch, window):
+@pytest.mark.parametrize("form", ["joined", "tiles"])
+def test_captured_step_follows_device_lengths(qd, kv, batch, window, form):
     """append + decode over the shared prefix, captured once on another stream
     and replayed as the sequences grow."""
     prefix, cap = 777, 130
@@ -194,6 +221,7 @@ def test_captured_step_follows_device_lengths(qd, kv, batch, window):
     nk, nv = torch.empty((batch, 256), device="cuda"), torch.empty((batch, 256), device="cuda")
     dst = torch.zeros(batch, dtype=torch.int64, device="cuda")
     out = torch.empty((batch, 8, 256), dtype=torch.float32, device="cuda")
+    kca.attn_force_path(kca.OP_PREFILL, FORMS[form])             # until the test ends (_unpinned)
     ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(kca.dtype_code(qt), kca.dtype_code(kt), prefix,
                                                                   [prefix + cap] * batch, window))
     stream = torch.cuda.Stream()
@@ -220,7 +248,9 @@ def test_captured_step_follows_device_lengths(qd, kv, batch, window):
     assert kca.attn_device_status(ws)[0] == 0
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("form", ["joined", "tiles"])
+def test_two_streams_at_once(form):
+    kca.attn_force_path(kca.OP_PREFILL, FORMS[form])
     cases = [("bf16", "bf16", 5, 4000), ("f32", "f16", 4, 3000)]
     streams = [torch.cuda.Stream() for _ in cases]
     sets = []
@@ -245,22 +275,60 @@ def test_two_streams_at_once():
 
 @pytest.mark.parametrize("qd,kv,batch", [("bf16", "bf16", 20), ("f32", "f16", 9), ("f32", "f32", 4), ("f16", "f16", 1)])
 @pytest.mark.parametrize("device", [False, True])
-def test_through_the_checked_build(qd, kv, batch, device):
+@pytest.mark.parametrize("form", ["joined", "tiles", "units"])
+def test_through_the_checked_build(qd, kv, batch, device, form):
     """The bounds-checked build records nothing and gives the same bits."""
     prefix, cap, window = 2500, 80, 1999
     data = _data(55, batch, prefix, cap, qd, kv)
     ctx = [prefix + int(c) for c in synth.integers(56, "c", 0, cap, batch)]
     codes = {"f32": kca.F32, "f16": kca.F16, "bf16": kca.BF16}
-    ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(codes[qd], codes[kv], prefix, [prefix + cap] * batch,
-                                                                  window))
-    a = _run(data, qd, kv, ctx, window, device=device, ws=ws)
+    with _form(form):
+        ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(codes[qd], codes[kv], prefix,
+                                                                      [prefix + cap] * batch, window))
+        a = _run(data, qd, kv, ctx, window, device=device, ws=ws)
     torch.cuda.synchronize()
     saved = kca._lib
     kca._lib = kca.load_library(kca.LIB_CHECKED_PATH)
     try:
-        b = _run(data, qd, kv, ctx, window, device=device, ws=ws)
+        with _form(form):
+            b = _run(data, qd, kv, ctx, window, device=device, ws=ws)
         torch.cuda.synchronize()
         assert kca.attn_device_status(ws)[0] == 0
     finally:
         kca._lib = saved
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("qd,kv,batch,prefix,cap", [("bf16", "bf16", 32, 9000, 700), ("f16", "f16", 100, 3000, 40),
+                                                    ("f16", "f16", 4, 3000, 20000), ("f32", "f16", 9, 2000, 5000)])
+@pytest.mark.parametrize("form", ["auto", "tiles"])
+@pytest.mark.parametrize("device", [False, True])
+def test_own_keys_beside_and_behind_the_prefix(qd, kv, batch, prefix, cap, form, device):
+    """Own keys of one or several clusters a sequence, on SMs that the prefix
+    leaves or after it; every sequence's merge takes the prefix's partials once."""
+    data = _data(57, batch, prefix, cap, qd, kv)
+    ctx = [prefix + int(c) for c in synth.integers(58, "c", 0, cap, batch)]
+    ctx[-1] = prefix + cap
+    with _form(form):
+        outs = [_run(data, qd, kv, ctx, device=device) for _ in range(3)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    _check(outs[0], "f32", data, qd, kv, ctx, 0, seqs=sorted({0, batch // 2, batch - 1}))
+
+
+@pytest.mark.parametrize("qd,kv", [("bf16", "bf16"), ("f32", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("form", ["auto", "joined", "tiles", "units"])
+@pytest.mark.parametrize("window", [0, 700])
+def test_one_workspace_for_every_shorter_length(qd, kv, form, window):
+    """Sized once for the bound, it serves host lengths up to it: ragged ones,
+    whose own plan needs more, and equal ones."""
+    prefix, cap, batch = 600, 30000, 6
+    data = _data(59, batch, prefix, cap, qd, kv)
+    codes = {"f32": kca.F32, "f16": kca.F16, "bf16": kca.BF16}
+    with _form(form):
+        ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(codes[qd], codes[kv], prefix,
+                                                                      [prefix + cap] * batch, window))
+        for own in ([30000, 1, 0, 64, 100, 3], [5] * batch, [30000] * batch, [0, 0, 0, 0, 0, 17000]):
+            ctx = [prefix + c for c in own]
+            got = _run(data, qd, kv, ctx, window, ws=ws)
+            _check(got, "f32", data, qd, kv, ctx, window)
+    assert kca.attn_device_status(ws)[0] == 0
