@@ -570,28 +570,30 @@ int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t b
     *out = p;
     return KCA_OK;
   }
-  // The routes' times in microseconds, from B200 graph replays: the decode
-  // kernel's estimate (mma_rows_plan) and 2 for a launch; or 8.5 for the
-  // tiles' and their 1.65 per 128 keys (17 and 1.1 per 64 keys for units), the
-  // own keys, and the partials' way through L2.  Measured, joined against
-  // tiles or units: 3 x 1,000 bf16 6.4 / 12.8, 8 x 8,192 of f32 queries 15.7 /
-  // 21.9, 32 x 16,384 bf16 66 / 19.3, 256 x 120,000 f16 3,389 / 204.
-  int joined_cluster = 0;
-  double t_joined = 0., t_own = 0.;
-  const kca::RowsPlan all = mma_rows_plan(batch, joined, sms, &joined_cluster, nullptr, &t_joined);
-  p.own = mma_rows_plan(batch, own, sms, &p.own_cluster, nullptr, &t_own);
-  if (joined_cluster < 1 || p.own_cluster < 1) return KCA_ERR_CUDA;
-  t_joined = 2. + 1e6 * t_joined;
-  t_own = 1e6 * t_own;
-  int64_t longest = 1;
-  for (int32_t b = 0; b < batch; ++b) longest = own[b] > longest ? own[b] : longest;
+  // The routes' times in microseconds, from B200 graph replays: 5 and the keys
+  // at 6.5 TB/s; or 8.5 for the tiles' launch and 1.65 per 128 keys (17 and 1.1
+  // per 64 keys for units), the own keys, and the partials' way through L2.
+  // Measured, joined against tiles or units: 3 x 1,000 bf16 6.4 / 12.8, 8 x
+  // 8,192 of f32 queries 15.7 / 21.9, 32 x 16,384 bf16 66 / 19.3, 256 x 120,000
+  // f16 3,389 / 204.
+  int64_t longest = 1, sum_own = 0, sum_joined = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    longest = own[b] > longest ? own[b] : longest;
+    sum_own += own[b];
+    sum_joined += joined[b];
+  }
+  const double t_joined = 5. + (double)sum_joined * 1024. / 6.5e6;
+  double t_own = 1.5 + (double)sum_own * 1024. / 6.5e6;
+  if (batch > sms / 2) {   // one CTA a sequence, in waves
+    const double waves = (double)((batch + sms - 1) / sms) * (double)longest * 1024. / 50e3;
+    if (waves > t_own) t_own = waves;
+  }
+  int cluster = 0;   // of the chosen form; 0: over the whole GPU
   size_t parts = 0;
   const int forced = g_prefill_path.load(std::memory_order_relaxed);
   double best = 0.;
   if (p.kv_lo < prefix_len && forced != 0) {
     p.route = q_dtype == kv_dtype && forced != 2 ? PrefixPlan::kTiles : PrefixPlan::kUnits;
-    const kca::RowsPlan own_all = p.own;
-    const int own_all_cluster = p.own_cluster;
     // c = 0: prefix and own keys each over the whole GPU, one after the other;
     // else each sequence's own keys on one cluster of c CTAs beside the
     // prefix, on SMs that it leaves (they run at once until the merge).
@@ -612,16 +614,15 @@ int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t b
         ur = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
         const int32_t units = (batch + ur - 1) / ur;
         if (units > left) continue;
-        int64_t nk[KCA_MAX_BATCH];
-        for (int32_t u = 0; u < units; ++u) nk[u] = prefix_len - p.kv_lo;
-        pre = kca::make_rows_plan(units, nk, left, kca::kMultiRowMinSplit);
+        pre = kca::make_equal_rows_plan(units, prefix_len - p.kv_lo, left, kca::kMultiRowMinSplit);
         bytes = slots_bytes((size_t)batch * pre.max_splits * kHeads);
         t = 17. + 1.1 * pre.split_len / kRowsStage;
       }
-      kca::RowsPlan o = own_all;
+      kca::RowsPlan o{};
       if (c == 0) {
         t += t_own;
       } else {
+        o.n_units = batch;
         o.split_len = (int32_t)(kca::cdiv(kca::cdiv(longest, c), kRowsStage) * kRowsStage);
         o.max_splits = kca::rows_n_splits(longest, o.split_len);
         const double t_beside = 2. + (double)o.split_len * 1024. / 50e3;
@@ -635,16 +636,18 @@ int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t b
       p.pre = pre;
       p.unit_rows = ur;
       p.own = o;
-      p.own_cluster = c == 0 ? own_all_cluster : c;
+      cluster = c;
     }
   }
   if (parts == 0 || (forced < 0 && t_joined <= best)) {
     p.route = PrefixPlan::kJoined;
-    p.own = all;
-    p.own_cluster = joined_cluster;
+    p.own = mma_rows_plan(batch, joined, sms, &p.own_cluster);
   } else {
     p.own_parts += parts;
+    p.own_cluster = cluster;
+    if (cluster == 0) p.own = mma_rows_plan(batch, own, sms, &p.own_cluster);
   }
+  if (p.own_cluster < 1) return KCA_ERR_CUDA;
   p.total = p.own_parts + mma_ws_bytes(p.own, p.own_cluster) - KCA_WORKSPACE_HEADER;
   *out = p;
   return KCA_OK;

@@ -103,6 +103,19 @@ inline RowsPlan make_rows_plan(int32_t n_units, const int64_t* nkeys, int32_t nu
   return p;
 }
 
+// The same for units of one length, without the search: num_sms / n_units
+// splits a unit.
+inline RowsPlan make_equal_rows_plan(int32_t n_units, int64_t nkeys, int32_t num_sms, int32_t min_split) {
+  RowsPlan p;
+  p.n_units = n_units;
+  const int64_t splits = num_sms > n_units ? num_sms / n_units : 1;
+  int64_t len = cdiv(cdiv(nkeys, splits), kRowsSplitQuantum) * kRowsSplitQuantum;
+  if (len < min_split) len = min_split;
+  p.split_len = (int32_t)len;
+  p.max_splits = rows_n_splits(nkeys, p.split_len);
+  return p;
+}
+
 // Tensor-core rows kernel: the splits of a unit run as clusters of `cluster`
 // CTAs (one CTA per SM), so a unit with n splits takes ceil(n / cluster)
 // clusters.  split_len is the smallest multiple of the kernel's stage
@@ -117,11 +130,21 @@ inline RowsPlan make_cluster_rows_plan(int32_t n_units, const int64_t* nkeys, in
   p.n_units = n_units;
   int64_t max_keys = 0;
   for (int32_t u = 0; u < n_units; ++u) max_keys = nkeys[u] > max_keys ? nkeys[u] : max_keys;
-  const int64_t c = cluster > 0 ? cluster : 1;
+  const uint32_t c = cluster > 0 ? (uint32_t)cluster : 1u;
   const int64_t target = slots > 0 ? slots : 1;
+  bool same = true;   // units of one length, the usual batch: counted once
+  for (int32_t u = 1; u < n_units; ++u) same = same && nkeys[u] == nkeys[0];
+  // Clusters of all units with splits of `len` keys (whole stages); any count
+  // past the target says as much as the exact one.
   auto count = [&](int64_t len) {
+    const uint32_t per = (uint32_t)(len / kRowsMmaStage);
     int64_t n = 0;
-    for (int32_t u = 0; u < n_units; ++u) n += cdiv(rows_n_splits(nkeys[u], (int32_t)len), c);
+    for (int32_t u = 0; u < n_units && n <= target; ++u) {
+      const uint32_t stages = nkeys[u] <= 0 ? 1u : (uint32_t)((nkeys[u] + kRowsMmaStage - 1) / kRowsMmaStage);
+      const uint32_t k = ((stages + per - 1) / per + c - 1) / c;
+      if (same) return (int64_t)k * n_units;
+      n += k;
+    }
     return n;
   };
   int64_t hi = cdiv(max_keys > kRowsMmaStage ? max_keys : kRowsMmaStage, kRowsMmaStage);
