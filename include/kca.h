@@ -445,8 +445,8 @@ int attn_dot_canary(void *stream, int32_t *variant);
  *                contiguous and of q_out_dtype (KCA_ERR_RANGE otherwise)
  *   k_cache/v_cache, kv_dtype, cache_rows, dst_rows_dev, dst_row0, workspace
  *                as in attn_append_kv, except that a device destination of -1
- *                marks a padding token: nothing of it is read or written
- *                (q_out included), and that is no error.  Any other
+ *                marks a padding token: nothing of it is written (q_out
+ *                included), and that is no error.  Any other
  *                destination outside the cache skips the token likewise and is
  *                recorded (error bit 3, value 4).
  * Returns KCA_OK or a KCA_ERR_* before launching anything.

@@ -8,22 +8,25 @@
 //             z[i + 128] = y[i + 128] cos a_i + y[i] sin a_i
 // then q to its own buffer and k, v to the cache rows the caller names.
 //
-// Bound: memory.  A token is 10 rows in and 10 out (10 KiB with 16-bit types)
-// against ~50 operations per element pair, so the pass over HBM decides for
-// many tokens, and the launch plus one chain of loads for few.  Hence one
-// warp holds HG rows of a token in registers from load to store (all loads
-// issued first), and the cosines and sines of a token are computed once per
-// warp, not read: a table of 131,072 positions would be 134 MB, and the 1 KiB
-// of it that a token needs another tenth of its traffic.
+// Bound: a token is 10 rows in and 10 out (10 KiB with 16-bit types) against
+// some 600 warp instructions, so for many tokens memory and instruction issue
+// are close, and for few the launch and one chain of loads decide.  Hence one
+// warp holds five rows of a token from load to store (all loads issued before
+// anything waits, the destination's own load among them), the norms and
+// rotations are taken on pairs, and the cosines and sines of a token are
+// computed, not read: a table of 131,072 positions would be 134 MB, and the
+// 1 KiB of it that a token needs another tenth of its traffic.
 //
 // Angles: pos * inv_freq can be 1e5 radians, where f32 has lost the fraction
 // of a turn, so the product is taken in f64 in turns (1 / 2 pi folded in), the
-// nearest whole turn subtracted there, and only the remainder (at most half a
-// turn) goes to f32.  Sums of squares, norms and rotations are f32; the one
-// rounding to fewer bits is the store.
+// nearest whole turn subtracted there, and only the remainder (at most an
+// eighth of a turn, after the nearest quarter) goes to f32.  Sums of squares,
+// norms and rotations are f32; the one rounding to fewer bits is the store.
 //
-// Rows per warp: 10 warps a token (one row each) while that fills no more
-// than the GPU's warps, else 2 (five rows each), which share the angles.
+// Measured on a B200: 1 token 2.4 us, 768 tokens 3.9, 16,384 tokens f32 into an
+// f16 cache 39.9 us (6.3 TB/s), bf16 32.5 us (5.2 TB/s).
+// Rows per warp: one (10 warps a token, which share no angle) up to 384 tokens,
+// five above (256 tokens: 3.3 us against 3.6; 512: 4.1 against 3.6).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -60,154 +63,217 @@ struct NormRopeArgs {
   uint32_t axis4[kHalf / 4];   // axis of frequency 4 i + j in byte j of word i
 };
 
-// Four consecutive elements from a 16-byte (f32) or 8-byte aligned address.
+// Four consecutive elements as they are stored (16-byte aligned for f32, else
+// 8-byte), and as two pairs.
 template <int DT>
-__device__ __forceinline__ void get4(const void* row, int dim, float* x) {
-  if (DT == KCA_F32) {
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + dim);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+struct Quad { using type = uint2; };
+template <>
+struct Quad<KCA_F32> { using type = float4; };
+template <int DT>
+__device__ __forceinline__ typename Quad<DT>::type load4(const void* row, int dim) {
+  return *reinterpret_cast<const typename Quad<DT>::type*>(static_cast<const char*>(row) + dim * ElemBytes<DT>::value);
+}
+template <int DT>
+__device__ __forceinline__ void pairs(const typename Quad<DT>::type& v, float2* x) {
+  if constexpr (DT == KCA_F32) {
+    x[0] = make_float2(v.x, v.y);
+    x[1] = make_float2(v.z, v.w);
   } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(row) + dim);
-    const uint32_t w[2] = {u.x, u.y};
+    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 f = DT == KCA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
-                                     : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 2; ++i)
+      x[i] = DT == KCA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
+                           : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
   }
 }
-__device__ __forceinline__ void get4(int dt, const void* row, int dim, float* x) {
-  if (dt == KCA_F32) get4<KCA_F32>(row, dim, x);
-  else if (dt == KCA_F16) get4<KCA_F16>(row, dim, x);
-  else get4<KCA_BF16>(row, dim, x);
+__device__ __forceinline__ void get4(int dt, const void* row, int dim, float2* x) {
+  if (dt == KCA_F32) pairs<KCA_F32>(load4<KCA_F32>(row, dim), x);
+  else if (dt == KCA_F16) pairs<KCA_F16>(load4<KCA_F16>(row, dim), x);
+  else pairs<KCA_BF16>(load4<KCA_BF16>(row, dim), x);
 }
-__device__ __forceinline__ void put4(int dt, void* row, int dim, const float* x) {
+__device__ __forceinline__ void put4(int dt, void* row, int dim, const float2* x) {
   if (dt == KCA_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(row) + dim) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(static_cast<float*>(row) + dim) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
     return;
   }
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (dt == KCA_F16) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      const __half2 h = __float22half2_rn(x[i]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 h = __float22bfloat162_rn(x[i]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
   *reinterpret_cast<uint2*>(static_cast<unsigned short*>(row) + dim) = make_uint2(w[0], w[1]);
 }
 
+// sin and cos of t turns, |t| <= 1/2: the nearest quarter turn off (exact), the
+// rest, at most pi / 4 radians, by the Taylor series (next terms x^11 / 11! and
+// x^12 / 12!: below 2^-29), the quarter by swapping and signs.
+__device__ __forceinline__ void sincos_turns(double t, float* s, float* c) {
+  const float f = (float)t;
+  const float k = rintf(4.f * f);
+  const float x = (float)(t - 0.25 * (double)k) * 6.283185307179586f, y = x * x;
+  float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
+  sn = fmaf(y, sn, 8.3333333e-3f);
+  sn = fmaf(y, sn, -1.6666667e-1f);
+  sn = fmaf(x * y, sn, x);
+  float cs = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);
+  cs = fmaf(y, cs, -1.3888889e-3f);
+  cs = fmaf(y, cs, 4.1666667e-2f);
+  cs = fmaf(y, cs, -0.5f);
+  cs = fmaf(y, cs, 1.f);
+  const int q = (int)k;   // -2 .. 2; a NaN stays one
+  const float a = q & 1 ? cs : sn, b = q & 1 ? sn : cs;
+  *s = q & 2 ? -a : a;
+  *c = (q + 1) & 2 ? -b : b;
+}
+
 // Weight and offset of a lane's eight dims: 1 where there is no weight.
-__device__ __forceinline__ void row_weight(const NormRopeArgs& a, const void* w, int d1, int d2, float (&wt)[8]) {
+__device__ __forceinline__ void row_weight(const NormRopeArgs& a, const void* w, int d1, int d2, float2 (&wt)[4]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wt[j] = 1.f;
+    for (int j = 0; j < 4; ++j) wt[j] = make_float2(1.f, 1.f);
     return;
   }
   get4(a.w_dtype, w, d1, wt);
-  get4(a.w_dtype, w, d2, wt + 4);
+  get4(a.w_dtype, w, d2, wt + 2);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) wt[j] += a.w0;
+  for (int j = 0; j < 4; ++j) wt[j] = __fadd2_rn(wt[j], make_float2(a.w0, a.w0));
 }
 
-// Lane l of a warp holds dims 4 l .. 4 l + 3 and 128 + 4 l .. + 3 of each of
-// its rows: the two halves of four rotation pairs, and 256- or 512-byte
-// contiguous accesses per warp.
-template <int IT, int HG>
-__global__ void __launch_bounds__(kNormWarps * 32, HG == 1 ? 1 : 4) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int kGroups = kTokenRows / HG;
+// A warp's part of a token: rows FIRST .. FIRST + HG - 1 (FIRST < 0: the one row
+// `row0`; known at compile time otherwise, which leaves a third of the
+// instructions: no choices by row, addresses at constant offsets).  OT: type of
+// q_out and of the cache, or -1 where they differ.
+// Lane l holds dims 4 l .. 4 l + 3 and 128 + 4 l .. + 3 of each of its rows: the
+// two halves of four rotation pairs, and 256- or 512-byte contiguous accesses
+// per warp.
+template <int IT, int OT, int HG, int FIRST>
+__device__ __forceinline__ void norm_rope_rows(const NormRopeArgs& a, int64_t token, int row0, int lane) {
   constexpr int kIn = ElemBytes<IT>::value;
-  const int64_t w = (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
-  const int64_t token = w / kGroups;
-  const int first = (int)(w % kGroups) * HG;
-  const int lane = threadIdx.x & 31;
-  // Programmatic dependent launch: nothing of the caller's is read before the
-  // previous kernel of the stream is done.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (token >= a.n_rows) return;
+  const int first = FIRST < 0 ? row0 : FIRST;
+  const int d1 = 4 * lane, d2 = kHalf + 4 * lane;
   const int64_t dst = a.dst != nullptr ? a.dst[token] : a.dst0 + token;
+  const char* q_in = static_cast<const char*>(a.q) + token * a.q_stride * kIn;
+  const char* k_in = static_cast<const char*>(a.k) + token * a.k_stride * kIn;
+  const char* v_in = static_cast<const char*>(a.v) + token * a.v_stride * kIn;
+  // dims d1 .. + 3 and d2 .. + 3 of each row, kept as stored: 16-bit rows are
+  // unpacked twice, which costs less than the registers of a second copy
+  typename Quad<IT>::type raw[HG][2];
+#pragma unroll
+  for (int i = 0; i < HG; ++i) {
+    const int r = first + i;
+    const char* row = r < kHeads ? q_in + r * kDim * kIn : r == kHeads ? k_in : v_in;
+    raw[i][0] = load4<IT>(row, d1);
+    raw[i][1] = load4<IT>(row, d2);
+  }
+  float2 c[2], s[2], ns[2];   // cosine, sine, -sine
+  const bool turn = a.pos != nullptr && first <= kHeads;   // a warp with only the value row needs no angle
+  if (turn) {
+    const float4 f4 = *reinterpret_cast<const float4*>(a.inv_freq + d1);
+    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+    double p[4];
+    if (a.n_axes == 1) {
+      p[0] = p[1] = p[2] = p[3] = (double)a.pos[token];
+    } else {
+      const uint32_t ax = a.axis4[lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = (double)a.pos[(int64_t)((ax >> (8 * i)) & 0xffu) * a.n_rows + token];
+    }
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double t = p[i] * (double)f[i] * 0.15915494309189533577;   // turns
+      sincos_turns(t - rint(t), &sn[i], &cs[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = make_float2(cs[2 * i], cs[2 * i + 1]);
+      s[i] = make_float2(sn[2 * i], sn[2 * i + 1]);
+      ns[i] = make_float2(-sn[2 * i], -sn[2 * i + 1]);
+    }
+  }
+  // The rows are on their way before the destination is looked at.
   if (dst < 0 || dst >= a.cache_rows) {
     // -1 marks a padding token; any other value outside the cache is an error
     if (dst != -1 && first == 0 && lane == 0) record_error(a.status, kSiteAppend, kErrBadRow, (unsigned)token);
     return;
   }
-  const int d1 = 4 * lane, d2 = kHalf + 4 * lane;
-  float x[HG][8];
-#pragma unroll
-  for (int i = 0; i < HG; ++i) {
-    const int r = first + i;
-    const char* row = r < kHeads    ? static_cast<const char*>(a.q) + (token * a.q_stride + r * kDim) * kIn
-                      : r == kHeads ? static_cast<const char*>(a.k) + token * a.k_stride * kIn
-                                    : static_cast<const char*>(a.v) + token * a.v_stride * kIn;
-    get4<IT>(row, d1, x[i]);
-    get4<IT>(row, d2, x[i] + 4);
-  }
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  const bool turn = a.pos != nullptr && first <= kHeads;   // a warp with only the value row needs no angle
-  if (turn) {
-    const float4 f4 = *reinterpret_cast<const float4*>(a.inv_freq + d1);
-    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-    int64_t p0 = a.pos[token];
-    const uint32_t ax = a.n_axes > 1 ? a.axis4[lane] : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t p = a.n_axes > 1 ? a.pos[(int64_t)((ax >> (8 * i)) & 0xffu) * a.n_rows + token] : p0;
-      double t = (double)p * (double)f[i] * 0.15915494309189533577;   // turns
-      t -= rint(t);
-      sincospif(2.f * (float)t, &s[i], &c[i]);
-    }
-  }
-  // Sums of squares of the warp's rows, then 1 / sqrt(mean + eps).
+  // Sums of squares of the warp's rows (all steps of the butterfly for one
+  // distance at a time: their latencies overlap).
   float rs[HG];
 #pragma unroll
   for (int i = 0; i < HG; ++i) {
-    float ss = 0.f;
+    float2 x[4];
+    pairs<IT>(raw[i][0], x);
+    pairs<IT>(raw[i][1], x + 2);
+    float2 ss = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
-    rs[i] = ss;
+    for (int j = 1; j < 4; ++j) ss = __ffma2_rn(x[j], x[j], ss);
+    rs[i] = ss.x + ss.y;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < HG; ++i) rs[i] += __shfl_xor_sync(0xffffffffu, rs[i], o);
-  float wt[8];   // the warp's query rows share one weight, read once
+  float2 wt[4];   // the warp's query rows share one weight, read once
   if (a.norm_qk && first < kHeads) row_weight(a, a.wq, d1, d2, wt);
 #pragma unroll
   for (int i = 0; i < HG; ++i) {
     const int r = first + i;
+    float2 x[4];
+    pairs<IT>(raw[i][0], x);
+    pairs<IT>(raw[i][1], x + 2);
     if (r < kTokenRows - 1 ? a.norm_qk : a.norm_v) {
       if (r == kHeads) row_weight(a, a.wk, d1, d2, wt);
-      const float f = 1.f / sqrtf(rs[i] * (1.f / kDim) + a.eps);
-      const bool weighted = r < kTokenRows - 1;
+      const float f = rsqrtf(rs[i] * (1.f / kDim) + a.eps);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = weighted ? x[i][j] * f * wt[j] : x[i][j] * f;
+      for (int j = 0; j < 4; ++j) {
+        x[j] = __fmul2_rn(x[j], make_float2(f, f));
+        if (r < kTokenRows - 1) x[j] = __fmul2_rn(x[j], wt[j]);
+      }
     }
     if (r <= kHeads && turn) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = x[i][j], hi = x[i][4 + j];
-        x[i][j] = lo * c[j] - hi * s[j];
-        x[i][4 + j] = hi * c[j] + lo * s[j];
+      for (int j = 0; j < 2; ++j) {
+        const float2 lo = x[j], hi = x[2 + j];
+        x[j] = __ffma2_rn(lo, c[j], __fmul2_rn(hi, ns[j]));
+        x[2 + j] = __ffma2_rn(hi, c[j], __fmul2_rn(lo, s[j]));
       }
     }
-    const int dt = r < kHeads ? a.q_dtype : a.kv_dtype;
+    const int dt = OT >= 0 ? OT : r < kHeads ? a.q_dtype : a.kv_dtype;
     const int esz = dt == KCA_F32 ? 4 : 2;
-    char* out = r < kHeads    ? static_cast<char*>(a.q_out) + (token * kHeads + r) * (kDim * esz)
+    char* out = r < kHeads    ? static_cast<char*>(a.q_out) + token * (kHeads * kDim * esz) + r * (kDim * esz)
                 : r == kHeads ? static_cast<char*>(a.k_cache) + dst * (kDim * esz)
                               : static_cast<char*>(a.v_cache) + dst * (kDim * esz);
-    put4(dt, out, d1, x[i]);
-    put4(dt, out, d2, x[i] + 4);
+    put4(dt, out, d1, x);
+    put4(dt, out, d2, x + 2);
   }
 }
 
-template <int IT, int HG>
+template <int IT, int OT, int HG>
+__global__ void __launch_bounds__(kNormWarps * 32, HG == 1 ? 1 : IT == KCA_F32 ? 3 : 4) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int kGroups = kTokenRows / HG;
+  const int64_t w = (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+  const int64_t token = w / kGroups;
+  const int group = (int)(w % kGroups), lane = threadIdx.x & 31;
+  // Programmatic dependent launch: nothing of the caller's is read before the
+  // previous kernel of the stream is done.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (token >= a.n_rows) return;
+  if constexpr (HG == 1) norm_rope_rows<IT, OT, 1, -1>(a, token, group, lane);
+  else if (group == 0) norm_rope_rows<IT, OT, HG, 0>(a, token, 0, lane);
+  else norm_rope_rows<IT, OT, HG, HG>(a, token, HG, lane);
+}
+
+template <int IT, int OT, int HG>
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
+  static_assert(HG == 1 || 2 * HG == kTokenRows, "a token is ten warps' rows or two's");
   const int64_t warps = (int64_t)a.n_rows * (kTokenRows / HG);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -218,14 +284,21 @@ cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<IT, HG>, a);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<IT, OT, HG>, a);
 }
 
 // Tokens up to which every row gets its own warp (10 warps a token).
-constexpr int kOneRowTokens = 512;
+constexpr int kOneRowTokens = 384;
+template <int IT, int OT>
+cudaError_t launch_out(const NormRopeArgs& a, cudaStream_t stream) {
+  return a.n_rows <= kOneRowTokens ? launch_t<IT, OT, 1>(a, stream) : launch_t<IT, OT, 5>(a, stream);
+}
 template <int IT>
 cudaError_t launch_in(const NormRopeArgs& a, cudaStream_t stream) {
-  return a.n_rows <= kOneRowTokens ? launch_t<IT, 1>(a, stream) : launch_t<IT, 5>(a, stream);
+  if (a.q_dtype != a.kv_dtype) return launch_out<IT, -1>(a, stream);
+  if (a.q_dtype == KCA_F32) return launch_out<IT, KCA_F32>(a, stream);
+  if (a.q_dtype == KCA_F16) return launch_out<IT, KCA_F16>(a, stream);
+  return launch_out<IT, KCA_BF16>(a, stream);
 }
 
 bool norm_dtype_ok(int32_t d) { return d == KCA_F32 || d == KCA_F16 || d == KCA_BF16; }

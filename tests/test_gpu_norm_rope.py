@@ -18,11 +18,11 @@ pytestmark = pytest.mark.gpu
 HALF_STEP = {"f32": (2.0 ** -24, 2.0 ** -150), "f16": (2.0 ** -11, 2.0 ** -25), "bf16": (2.0 ** -8, 2.0 ** -134)}
 # The f32 computation, relative to the length of a rotated pair: the sum of
 # squares (8 fused steps and 5 additions of positive terms: 13 roundings, half
-# of them after the root), the mean, eps, root and quotient (4), two products
-# for the weight and its offset (3), the angle (a remainder of at most half a
-# turn rounded to f32 and doubled: 2 pi 2^-26 a rounding, 1.6; sincospif 2 ulp
-# of at most 2^-24 each: 4), and the products and sum of the rotation (3, by
-# sqrt 2): below 26 roundings of 2^-24.
+# of them after the root), the mean, eps and reciprocal root (2 ulp: 4), two
+# products for the weight and its offset (3), the angle (a remainder of at most
+# an eighth of a turn, rounded and scaled: 3 roundings of at most pi / 4; two
+# series: 2 each), and the products and sum of the rotation (3, by sqrt 2):
+# below 26 roundings of 2^-24.
 COMPUTE = 26 * 2.0 ** -24
 
 
