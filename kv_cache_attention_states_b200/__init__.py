@@ -191,19 +191,22 @@ def _check(status: int, what: str):
         raise KcaError(status, what)
 
 
-def _run(index: int, what: str, stream, *args):
-    """Calls entry point `what` on device `index` (the library works on the
-    current device) with the given arguments and the cudaStream_t of `stream`
-    (None: torch's current one), and raises on a status other than KCA_OK."""
+def _cuda_stream(stream, index: int) -> int:
+    """cudaStream_t of `stream`, or of torch's current stream on device `index`."""
     import torch
-    C = torch._C
-    s = C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _run(index: int, what: str, args: tuple):
+    """Calls entry point `what` on device `index` (the library works on the
+    current device) and raises on a status other than KCA_OK."""
+    import torch
     f = getattr(_lib or lib(), what)
-    if C._cuda_getDevice() == index:
-        st = f(*args, s)
+    if torch._C._cuda_getDevice() == index:
+        st = f(*args)
     else:
         with torch.cuda.device(index):
-            st = f(*args, s)
+            st = f(*args)
     if st != 0:
         raise KcaError(st, what)
 
@@ -551,15 +554,14 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
         raise ValueError("q must be [n, 8, 256] with each token's values contiguous")
     in_dtype, row, row1 = q.dtype, (n, HEAD_DIM), (n, 1, HEAD_DIM)
     k_stride, v_stride = k_new.stride(), v_new.stride()
-    for name, t, st in (("k_new", k_new, k_stride), ("v_new", v_new, v_stride)):
-        shape = t.shape
-        if t.get_device() != dev or t.dtype is not in_dtype or (shape != row and shape != row1) or st[-1] != 1:
-            raise ValueError(f"{name} must be [n, 256] of q's dtype on {q.device}, each token's values contiguous")
+    k_shape, v_shape = k_new.shape, v_new.shape
+    if ((k_shape != row and k_shape != row1) or (v_shape != row and v_shape != row1) or k_stride[-1] != 1
+            or v_stride[-1] != 1 or k_new.dtype is not in_dtype or v_new.dtype is not in_dtype
+            or k_new.get_device() != dev or v_new.get_device() != dev):
+        raise ValueError(f"k_new and v_new must be [n, 256] of q's dtype on {q.device}, each token's values contiguous")
     if (k_cache.get_device() != dev or not k_cache.is_contiguous() or v_cache.get_device() != dev
-            or not v_cache.is_contiguous() or _off(positions, dev) or _off(inv_freq, dev) or _off(q_weight, dev)
-            or _off(k_weight, dev) or _off(q_out, dev) or _off(workspace, dev)):
-        _need(q.device, k_cache=k_cache, v_cache=v_cache, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
-              k_weight=k_weight, q_out=q_out, workspace=workspace)
+            or not v_cache.is_contiguous() or (workspace is not None and _off(workspace, dev))):
+        _need(q.device, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
     shape = k_cache.shape
     if shape != v_cache.shape or shape[-1] != HEAD_DIM or k_cache.dtype is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must be alike, with a last axis of 256")
@@ -570,6 +572,9 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
         shape = positions.shape
         if len(shape) == 2:
             n_axes = shape[0]
+        if (positions.get_device() != dev or not positions.is_contiguous() or inv_freq.get_device() != dev
+                or not inv_freq.is_contiguous()):
+            _need(q.device, positions=positions, inv_freq=inv_freq)
         if positions.dtype is not torch.int64 or (shape != (n_axes, n) and shape != (n,)):
             raise ValueError("positions must be int64 [n] or [axes, n]")
         if inv_freq.dtype is not torch.float32 or inv_freq.numel() != HEAD_DIM // 2:
@@ -580,28 +585,33 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
     wt = k_weight if q_weight is None else q_weight
     wq_p = wk_p = None
     if q_weight is not None:
-        if q_weight.numel() != HEAD_DIM:
+        if q_weight.numel() != HEAD_DIM or q_weight.get_device() != dev or not q_weight.is_contiguous():
+            _need(q.device, q_weight=q_weight)
             raise ValueError("q_weight must be [256]")
         wq_p = q_weight.data_ptr()
     if k_weight is not None:
-        if k_weight.numel() != HEAD_DIM or k_weight.dtype is not wt.dtype:
+        if (k_weight.numel() != HEAD_DIM or k_weight.dtype is not wt.dtype or k_weight.get_device() != dev
+                or not k_weight.is_contiguous()):
+            _need(q.device, k_weight=k_weight)
             raise ValueError("q_weight and k_weight must be [256] of one dtype")
         wk_p = k_weight.data_ptr()
     if q_out is None:
         q_out = torch.empty((n, N_Q_HEADS, HEAD_DIM), dtype=k_cache.dtype, device=q.device)
-    elif q_out.numel() != n * N_Q_HEADS * HEAD_DIM:
+    elif (q_out.numel() != n * N_Q_HEADS * HEAD_DIM or q_out.get_device() != dev or not q_out.is_contiguous()):
+        _need(q.device, q_out=q_out)
         raise ValueError("q_out must be [n, 8, 256]")
     if isinstance(dst, int):
         dst_p, dst0 = None, dst
     else:
-        if dst.dtype is not torch.int64 or dst.numel() != n or _off(dst, dev):
+        if (dst.dtype is not torch.int64 or dst.numel() != n or dst.get_device() != dev or not dst.is_contiguous()):
             raise ValueError("dst must be an int or a contiguous int64 CUDA tensor [n]")
         dst_p, dst0 = dst.data_ptr(), 0
-    _run(dev, "attn_norm_rope_append", stream, q.data_ptr(), q_stride[0], k_new.data_ptr(), k_stride[0],
-         v_new.data_ptr(), v_stride[0], dtype_code(q), n, (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), wq_p,
-         wk_p, F32 if wt is None else dtype_code(wt), weight_offset, eps, pos_p, n_axes, _freq_axis(freq_axis, n_axes),
-         inv_p, q_out.data_ptr(), dtype_code(q_out), k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache),
-         k_cache.numel() // HEAD_DIM, dst_p, dst0, _ptr(workspace))
+    _run(dev, "attn_norm_rope_append", (
+        q.data_ptr(), q_stride[0], k_new.data_ptr(), k_stride[0], v_new.data_ptr(), v_stride[0], dtype_code(q), n,
+        (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), wq_p, wk_p, F32 if wt is None else dtype_code(wt),
+        weight_offset, eps, pos_p, n_axes, _freq_axis(freq_axis, n_axes), inv_p, q_out.data_ptr(), dtype_code(q_out),
+        k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.numel() // HEAD_DIM, dst_p, dst0,
+        _ptr(workspace), _cuda_stream(stream, dev)))
     return q_out
 
 
@@ -611,10 +621,11 @@ def _out_dtype(q, out):
     """`out`, or a new float32 tensor of q's shape, and its dtype code."""
     import torch
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    elif out.numel() != q.numel() or (out.dtype != q.dtype and out.dtype is not torch.float32):
+        return torch.empty(q.shape, dtype=torch.float32, device=q.device), F32
+    dt = out.dtype
+    if out.numel() != q.numel() or (dt is not q.dtype and dt is not torch.float32):
         raise ValueError("out must have q's shape and be float32 or of q's dtype")
-    return out, dtype_code(out)
+    return out, F32 if dt is torch.float32 else dtype_code(out)
 
 
 def _device_lengths(ctx_len_dev, batch: int):
@@ -665,7 +676,8 @@ def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache,
         raise ValueError("tensors must be CUDA tensors")
     batch = _queries(q)
     on_device = hasattr(ctx_len, "is_cuda") and ctx_len.is_cuda
-    if (_off(q, dev) or _off(prefix_k, dev) or _off(prefix_v, dev) or _off(k_cache, dev) or _off(v_cache, dev)
+    if (not q.is_contiguous() or _off(prefix_k, dev) or _off(prefix_v, dev) or k_cache.get_device() != dev
+            or not k_cache.is_contiguous() or v_cache.get_device() != dev or not v_cache.is_contiguous()
             or _off(out, dev) or _off(workspace, dev) or (on_device and _off(ctx_len, dev))):
         _need(q.device, q=q, prefix_k=prefix_k, prefix_v=prefix_v, k_cache=k_cache, v_cache=v_cache, out=out,
               workspace=workspace, ctx_len=ctx_len if on_device else None)
@@ -697,9 +709,10 @@ def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache,
         with torch.cuda.device(dev):
             workspace = new_workspace(attn_decode_prefix_workspace_bytes(
                 qd, kd, prefix_len, [ctx_bound] * batch if on_device else ctx_len, window), q.device, stream)
-    _run(dev, "attn_decode_prefix", stream, q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(),
-         v_cache.data_ptr(), kd, N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p, dev_p, ctx_bound, window, scale,
-         out.data_ptr(), od, workspace.data_ptr(), workspace.numel())
+    _run(dev, "attn_decode_prefix", (
+        q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(), v_cache.data_ptr(), kd,
+        N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p, dev_p, ctx_bound, window, scale, out.data_ptr(), od,
+        workspace.data_ptr(), workspace.numel(), _cuda_stream(stream, dev)))
     return out
 
 
@@ -723,7 +736,9 @@ def attn_summarize_blocks(k_cache, ctx_len_dev, n_new: int, codes=None, scales=N
         codes = torch.zeros((batch, blocks, 2, HEAD_DIM), dtype=torch.int8, device=k_cache.device)
     if scales is None:
         scales = torch.zeros((batch, blocks), dtype=torch.float32, device=k_cache.device)
-    if (_off(k_cache, dev) or _off(ctx_len_dev, dev) or _off(codes, dev) or _off(scales, dev) or _off(workspace, dev)):
+    if (not k_cache.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
+            or codes.get_device() != dev or not codes.is_contiguous() or scales.get_device() != dev
+            or not scales.is_contiguous() or _off(workspace, dev)):
         _need(k_cache.device, k_cache=k_cache, ctx_len_dev=ctx_len_dev, codes=codes, scales=scales, workspace=workspace)
     _device_lengths(ctx_len_dev, batch)
     if k_cache.numel() != batch * capacity * HEAD_DIM:
@@ -732,8 +747,9 @@ def attn_summarize_blocks(k_cache, ctx_len_dev, n_new: int, codes=None, scales=N
         raise ValueError("codes must be int8 [batch, ceil(capacity / 64), 2, 256]")
     if scales.dtype is not torch.float32 or scales.numel() != batch * blocks:
         raise ValueError("scales must be float32 [batch, ceil(capacity / 64)]")
-    _run(dev, "attn_summarize_blocks", stream, k_cache.data_ptr(), dtype_code(k_cache), capacity, batch, ctx_len_dev.data_ptr(),
-         n_new, codes.data_ptr(), scales.data_ptr(), _ptr(workspace))
+    _run(dev, "attn_summarize_blocks", (
+        k_cache.data_ptr(), dtype_code(k_cache), capacity, batch, ctx_len_dev.data_ptr(), n_new, codes.data_ptr(),
+        scales.data_ptr(), _ptr(workspace), _cuda_stream(stream, dev)))
     return codes, scales
 
 
@@ -760,8 +776,9 @@ def attn_select_blocks(q, codes, scales, ctx_len_dev, ctx_bound: int, n_select: 
     batch = _queries(q)
     if blocks is None:
         blocks = torch.empty((batch, n_select), dtype=torch.int32, device=q.device)
-    if (_off(q, dev) or _off(codes, dev) or _off(scales, dev) or _off(ctx_len_dev, dev) or _off(blocks, dev)
-            or _off(workspace, dev)):
+    if (not q.is_contiguous() or codes.get_device() != dev or not codes.is_contiguous() or scales.get_device() != dev
+            or not scales.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
+            or blocks.get_device() != dev or not blocks.is_contiguous() or _off(workspace, dev)):
         _need(q.device, q=q, codes=codes, scales=scales, ctx_len_dev=ctx_len_dev, blocks=blocks, workspace=workspace)
     _device_lengths(ctx_len_dev, batch)
     shape = scales.shape
@@ -773,9 +790,10 @@ def attn_select_blocks(q, codes, scales, ctx_len_dev, ctx_bound: int, n_select: 
     if workspace is None:
         with torch.cuda.device(dev):
             workspace = new_workspace(attn_select_blocks_workspace_bytes(batch, ctx_bound), q.device, stream)
-    _run(dev, "attn_select_blocks", stream, q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), shape[1],
-         batch, ctx_len_dev.data_ptr(), ctx_bound, n_select, n_sink, n_recent, blocks.data_ptr(), workspace.data_ptr(),
-         workspace.numel())
+    _run(dev, "attn_select_blocks", (
+        q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), shape[1], batch, ctx_len_dev.data_ptr(),
+        ctx_bound, n_select, n_sink, n_recent, blocks.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _cuda_stream(stream, dev)))
     return blocks
 
 
@@ -800,7 +818,9 @@ def attn_decode_blocks(q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound: int,
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
     batch = _queries(q)
-    if (_off(q, dev) or _off(k_cache, dev) or _off(v_cache, dev) or _off(blocks, dev) or _off(ctx_len_dev, dev)
+    if (not q.is_contiguous() or k_cache.get_device() != dev or not k_cache.is_contiguous()
+            or v_cache.get_device() != dev or not v_cache.is_contiguous() or blocks.get_device() != dev
+            or not blocks.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
             or _off(out, dev) or _off(workspace, dev)):
         _need(q.device, q=q, k_cache=k_cache, v_cache=v_cache, blocks=blocks, ctx_len_dev=ctx_len_dev, out=out,
               workspace=workspace)
@@ -816,9 +836,10 @@ def attn_decode_blocks(q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound: int,
     if workspace is None:
         with torch.cuda.device(dev):
             workspace = new_workspace(attn_decode_blocks_workspace_bytes(batch, n_list), q.device, stream)
-    _run(dev, "attn_decode_blocks", stream, q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(),
-         dtype_code(k_cache), N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, blocks.data_ptr(), n_list,
-         ctx_len_dev.data_ptr(), ctx_bound, scale, out.data_ptr(), od, workspace.data_ptr(), workspace.numel())
+    _run(dev, "attn_decode_blocks", (
+        q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), N_Q_HEADS,
+        N_KV_HEADS, HEAD_DIM, capacity, batch, blocks.data_ptr(), n_list, ctx_len_dev.data_ptr(), ctx_bound, scale,
+        out.data_ptr(), od, workspace.data_ptr(), workspace.numel(), _cuda_stream(stream, dev)))
     return out
 
 
