@@ -688,7 +688,8 @@ int attn_decode_cluster_capacity(int32_t *capacity);
  * process-wide, so that two paths can be compared on the same inputs (tests,
  * diagnosis).  op 0 (prefill): path 0 = the rows path, 1 = the tensor-core
  * path where eligible (q and cache both F16 or both BF16), 2 = multi-row
- * units where eligible (16-bit cache, 2-15 rows).  op 1 (the rows
+ * units where eligible (16-bit cache, 2-15 rows); it pins the form of
+ * attn_decode_prefix too, as described there.  op 1 (the rows
  * path: decode, and prefill chunks on the rows path): path 0 = the CUDA-core
  * kernel, 1 = the tensor-core (mma.sync) kernel where eligible (16-bit
  * cache).  op 2 (attn_prefill_batch with 2 or more rows per sequence on a

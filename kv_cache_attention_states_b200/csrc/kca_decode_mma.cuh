@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
   DeviceStatus* status = reinterpret_cast<DeviceStatus*>(a.status);
 
   const int C = a.cluster;                 // CTAs per cluster along the splits (1, 2, 4 or 8)
-  const int unit = blockIdx.y;
+  const int unit = kOwn ? a.order[blockIdx.y] : blockIdx.y;
   const int split = blockIdx.x;
   const int rank = split % C, clus = split / C;
   const int warp = threadIdx.x >> 5;

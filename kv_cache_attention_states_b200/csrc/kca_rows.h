@@ -88,6 +88,9 @@ struct RowsArgs {
   int32_t pre_group;
   int32_t pre_items;
   float pre_mscale;
+  // The unit that CTA row y of the grid takes (kSrcOwn): with more sequences
+  // than SMs the longest first, so that none is left for the end.
+  uint8_t order[KCA_MAX_BATCH];
 };
 
 // Rows of one unit of the batched multi-row kernels: 4 (both kernels), or 8
