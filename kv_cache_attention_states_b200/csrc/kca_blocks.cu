@@ -1,8 +1,8 @@
 // kca_blocks.cu -- the two steps before attention over selected key blocks:
 // bounds of every finished block of 64 keys (attn_summarize_blocks), and the
 // choice of a query's blocks by a cheap score (attn_select_blocks).  The
-// attention over the chosen blocks is the decode kernels' own (mode kBlocks
-// of kca_decode_mma.cu and kca_rows.cu).
+// attention over the chosen blocks is the decode kernels' own (kSrcBlocks of
+// kca_decode_mma.cuh and kca_rows.cu).
 //
 // Bounds.  For block j and dim t, hi = max and lo = min of K over the 64 keys;
 // a query value q then meets no key value above max(q hi, q lo), and
@@ -44,7 +44,8 @@ __device__ __forceinline__ uint32_t block_code(float x, float sx) {
 // the warps' bounds meet in shared memory, and the threads quantise them.
 // 16-bit keys stay packed until then: two values per maximum, and half the
 // exchange.
-// Bound: memory (32 KiB of 16-bit keys in, 516 bytes out).
+// Bound: memory (32 KiB of 16-bit keys in, 516 bytes out): 8,192 blocks of bf16
+// keys in 41.4 us on a B200, 6.5 TB/s; one step of 64 sequences 2.2 us.
 struct SummaryArgs {
   const void* k;
   const int64_t* ctx;
@@ -182,10 +183,13 @@ __global__ void __launch_bounds__(256) summarize_kernel(const SummaryArgs a) {
 // 2,048 bins over the span of the keys (not over their leading bits, which
 // scores share: their counts would all meet in a few words) finds the bin of
 // the smallest key taken; the search goes on inside that bin until it is
-// taken whole or holds one value -- one or two rounds for scores that differ.
+// taken whole or holds one value -- one or two rounds, of 1 us, for scores that
+// differ.
 // Two counts in index order place the blocks.
 // Bound: latency (516 bytes a block: 1 MB for 131,072 keys), hence many small
-// CTAs and one launch.
+// CTAs and one launch.  Measured on a B200: 6.2 us for 64 of 2,048 blocks of one
+// sequence (4.9 where nothing is to be searched), 9.1 us for 128 of up to 512
+// blocks of 32 sequences.
 constexpr int kSelThreads = 256;
 constexpr int kSelBlocks = 64;                       // blocks scored per CTA
 constexpr int kSelPer = KCA_MAX_BLOCKS / kSelThreads;  // scores per thread in the choice, and bins

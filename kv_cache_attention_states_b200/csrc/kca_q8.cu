@@ -2,7 +2,7 @@
 // canary.  K rows are stored as int8 codes with a per-row scale; the decode
 // kernels quantise the query the same way per head and take QK exactly on
 // the codes -- on int8 tensor-core MMAs in the decode kernel for 16-bit V
-// (kca_decode_mma.cu), four int8 pairs per dp4a on the CUDA cores for f32 V
+// (kca_decode_mma.cuh), four int8 pairs per dp4a on the CUDA cores for f32 V
 // (kca_rows.cu) -- then the softmax and V sum in f32.
 //
 // Prior art on the pages (Karume v0.8.0 release notes, "Fixes"): attention's

@@ -293,7 +293,7 @@ cudaError_t launch_multirow_merge(const RowsArgs& a, cudaStream_t stream);
 // once (0 on failure).
 int decode_mma_cluster_capacity(int c);
 
-// Tensor-core variant for 16-bit K/V (kca_decode_mma.cu); tmk / tmv map the
+// Tensor-core variant for 16-bit K/V (kca_decode_mma.cuh); tmk / tmv map the
 // cache rows [rows][256] with 64 x 64 boxes and 128-byte swizzle.  Merges in
 // the same kernel (clusters + tickets).
 cudaError_t launch_decode_mma(int q_dtype, int kv_dtype, const CUtensorMap& tmk, const CUtensorMap& tmv,
