@@ -9,8 +9,9 @@ import torch
 import kv_cache_attention_states_b200 as kca
 from kv_cache_attention_states_b200 import synth
 from oracle import blocks as ob
+from oracle import prefix as op
 from tests.helpers import dev
-from tests.helpers_bounds import f32_grade, rounded
+from tests.helpers_bounds import f32_grade, rounded, rounded_probabilities
 
 pytestmark = pytest.mark.gpu
 
@@ -355,3 +356,54 @@ def test_decode_blocks_through_the_checked_build(kv, n_list):
     finally:
         kca._lib = saved
     assert torch.equal(a, b)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured steps of two sizes -- blocks of one, a shared prefix of the other
+    -- replayed in turn on one stream over one workspace."""
+    cap = 64 * 60
+    q, k, v = _data(31, 4, cap, "f16", "f16")
+    codes, scales = _summ(31, 4, cap)
+    ctx = [cap, 700, 64, 3000]
+    t = dev(q, "f16"), dev(k, "f16"), dev(v, "f16"), torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    cd, pctx = _i64(ctx), _i64([cap + 500] * 4)
+    ws = kca.new_workspace(max(kca.attn_select_blocks_workspace_bytes(4, cap), kca.attn_decode_blocks_workspace_bytes(4, 40),
+                               kca.attn_decode_prefix_workspace_bytes(kca.F16, kca.F16, cap, [cap + cap] * 4)))
+    blocks = torch.empty((4, 40), dtype=torch.int32, device="cuda")
+    o1, o2 = (torch.empty((4, 8, 256), dtype=torch.float32, device="cuda") for _ in range(2))
+    stream = torch.cuda.Stream()
+
+    def choose():
+        kca.attn_select_blocks(t[0], t[3], t[4], cd, cap, 40, blocks=blocks, workspace=ws, stream=stream)
+        kca.attn_decode_blocks(t[0], t[1], t[2], blocks, cd, cap, out=o1, workspace=ws, stream=stream)
+
+    def behind():
+        kca.attn_decode_prefix(t[0], t[1][0], t[2][0], cap, t[1], t[2], pctx, ctx_bound=cap + cap, out=o2, workspace=ws,
+                               stream=stream)
+
+    graphs = []
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        choose()
+        behind()
+        stream.synchronize()
+        for f in (choose, behind):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                f()
+            graphs.append(g)
+        seen = []
+        for _ in range(8):
+            for g in graphs:
+                g.replay()
+            seen.append((blocks.clone(), o1.clone(), o2.clone()))
+    torch.cuda.synchronize()
+    lists = _want(q, "f16", codes, scales, ctx, 40)
+    assert np.array_equal(seen[0][0].cpu().numpy(), lists)
+    _check_out(seen[0][1], "f32", q, "f16", k, v, "f16", lists, ctx)
+    assert all(all(torch.equal(a, b) for a, b in zip(s, seen[0])) for s in seen)
+    want = [op.attend(q[b], "f16", k[0], v[0], k[b], v[b], "f16", cap + 500) for b in range(4)]
+    got = seen[0][2].cpu().numpy().astype(np.float64)
+    for b, (w, absqk, vmax, pabsv, n) in enumerate(want):
+        assert np.all(np.abs(got[b] - w) <= rounded(w, rounded_probabilities("f16", absqk, vmax, pabsv, n), "f32"))
+    assert kca.attn_device_status(ws)[0] == 0

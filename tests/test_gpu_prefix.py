@@ -332,3 +332,46 @@ def test_one_workspace_for_every_shorter_length(qd, kv, form, window):
             got = _run(data, qd, kv, ctx, window, ws=ws)
             _check(got, "f32", data, qd, kv, ctx, window)
     assert kca.attn_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("qd,kv,batch", [("bf16", "bf16", 40), ("f16", "f16", 4), ("f32", "f16", 10)])
+@pytest.mark.parametrize("form", ["tiles", "units", "joined"])
+@pytest.mark.parametrize("device", [False, True])
+def test_back_to_back_steps_see_their_own_inputs(qd, kv, batch, form, device):
+    """Steps queued without a pause -- queries, lengths and the newest key and
+    value written by the kernels just before each call -- give the bits that
+    the same steps give with the GPU waited for in between."""
+    prefix, cap, steps = 3000, 400, 60
+    data = _data(60, batch, prefix, cap, qd, kv)
+    pk, pv = dev(data[1], kv), dev(data[2], kv)
+    k0, v0 = dev(data[3], kv), dev(data[4], kv)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    qs = torch.randn((steps, batch, 8, 256), generator=gen, device="cuda").to(synth.torch_dtype(qd))
+    nk, nv = (torch.randn((steps, batch, 256), generator=gen, device="cuda") for _ in range(2))
+    lens = torch.stack([_i64([prefix + 300 + (t + 7 * b) % 90 for b in range(batch)]) for t in range(steps)])
+    host = lens.tolist()
+    rows = lens - prefix - 1 + torch.arange(batch, device="cuda") * cap
+    codes = {"f32": kca.F32, "f16": kca.F16, "bf16": kca.BF16}
+    results = []
+    with _form(form):
+        ws = kca.new_workspace(kca.attn_decode_prefix_workspace_bytes(codes[qd], codes[kv], prefix,
+                                                                      [prefix + cap] * batch))
+        for wait in (True, False):
+            k, v, q = k0.clone(), v0.clone(), torch.empty_like(qs[0])
+            ctx, dst = torch.empty_like(lens[0]), torch.empty_like(rows[0])
+            outs = torch.empty((steps, batch, 8, 256), dtype=torch.float32, device="cuda")
+            torch.cuda.synchronize()
+            for t in range(steps):
+                ctx.copy_(lens[t])
+                dst.copy_(rows[t])
+                q.copy_(qs[t])
+                kca.attn_append_kv(nk[t], nv[t], k.view(-1, 256), v.view(-1, 256), dst)
+                if wait:
+                    torch.cuda.synchronize()
+                kca.attn_decode_prefix(q, pk, pv, prefix, k, v, ctx if device else host[t], out=outs[t], workspace=ws)
+                if wait:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            results.append(outs)
+    assert torch.equal(results[0], results[1])
+    assert kca.attn_device_status(ws)[0] == 0
