@@ -1,10 +1,12 @@
 """B200-native states-form KV-cache attention (chunked causal prefill and
 split-context decode, 8 query heads sharing one KV head, head_dim 256).
 
-Thin ctypes binding over libkca.so, whose C ABI is declared in
-include/kca.h.  The functions keep the C names and only marshal arguments:
-torch tensors become device pointers, dtypes become codes, the current torch
-stream becomes the cudaStream_t.  Every step of the attention runs in the
+Thin binding over libkca.so, whose C ABI is declared in include/kca.h.  The
+functions keep the C names and only marshal arguments: torch tensors become
+device pointers, dtypes become codes, the current torch stream becomes the
+cudaStream_t.  Most do so through ctypes; the calls around the cache that are
+shorter than that (norm + rotation + append, shared prefix, selected blocks)
+through _kca_torch.so (csrc/kca_torch.cpp).  Every step of the attention runs in the
 library's CUDA kernels; there is no fallback, and a missing or unloadable
 library raises.
 """
@@ -19,6 +21,7 @@ from . import synth  # noqa: F401  (seeded inputs; no attention arithmetic)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkca.so")
+BINDING_PATH = os.path.join(_HERE, "_kca_torch.so")
 
 F32, F16, BF16, I8 = 0, 1, 2, 3
 I8_ROW_BYTES = 272        # packed int8 K row: 256 codes, f32 scale, 12 zero bytes
@@ -131,6 +134,7 @@ def load_library(path: str) -> ctypes.CDLL:
     L.attn_decode_blocks.restype = ctypes.c_int
     L.attn_decode_blocks_workspace_bytes.argtypes = [i32, i32]
     L.attn_decode_blocks_workspace_bytes.restype = sz
+    L.entries = {}   # addresses of entry points, for _kca_torch.so
     L.attn_force_path.argtypes = [i32, i32]
     L.attn_force_path.restype = ctypes.c_int
     L.attn_status_string.argtypes = [ctypes.c_int]
@@ -191,41 +195,46 @@ def _check(status: int, what: str):
         raise KcaError(status, what)
 
 
-def _cuda_stream(stream, index: int) -> int:
-    """cudaStream_t of `stream`, or of torch's current stream on device `index`."""
+_native = None
+
+
+def _calls():
+    """_kca_torch.so, which checks the tensors of a call and makes it."""
+    global _native
+    if _native is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, which the module links)
+        spec = importlib.util.spec_from_file_location("_kca_torch", BINDING_PATH)
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is missing: build it with python -m kv_cache_attention_states_b200.build")
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
+
+
+def _entry(name: str) -> int:
+    """Address of entry point `name` of the loaded library."""
+    L = _lib or lib()
+    address = L.entries.get(name)
+    if address is None:
+        address = L.entries[name] = ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+    return address
+
+
+def _f32_like(q):
     import torch
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return q.new_empty(q.shape, dtype=torch.float32)
 
 
-def _run(index: int, what: str, args: tuple):
-    """Calls entry point `what` on device `index` (the library works on the
-    current device) and raises on a status other than KCA_OK."""
+def _workspace_for(q, nbytes, stream):
+    """A new workspace of nbytes() bytes on q's device."""
     import torch
-    f = getattr(_lib or lib(), what)
-    if torch._C._cuda_getDevice() == index:
-        st = f(*args)
-    else:
-        with torch.cuda.device(index):
-            st = f(*args)
-    if st != 0:
-        raise KcaError(st, what)
-
-
-def _need(device, **tensors):
-    """Names the tensor (None is skipped) that is not contiguous on `device`.
-    The calls test all of theirs in one condition and come here when it fails."""
-    for name, t in tensors.items():
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous tensor on {device}")
-
-
-def _off(t, index: int) -> bool:
-    """Whether t is anything but contiguous on device `index` (None: no)."""
-    return t is not None and (t.get_device() != index or not t.is_contiguous())
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    if not q.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    with torch.cuda.device(q.device):
+        return new_workspace(nbytes(), q.device, stream)
 
 
 # ----------------------------------------------------------------- workspace
@@ -509,25 +518,6 @@ def attn_append_kv(k_new, v_new, k_cache, v_cache, dst, rope_cos=None, rope_sin=
     _check(st, "attn_append_kv")
 
 
-_FREQ_AXIS = {}
-
-
-def _freq_axis(freq_axis, n_axes: int):
-    """The axis of each of the 128 frequencies as a C byte array (checked and
-    made once per distinct assignment), or None."""
-    if freq_axis is None:
-        return None
-    key = bytes(freq_axis)
-    arr = _FREQ_AXIS.get((key, n_axes))
-    if arr is None:
-        if len(key) != HEAD_DIM // 2 or max(key) >= n_axes:
-            raise ValueError(f"freq_axis must give one of {n_axes} axes for each of 128 frequencies")
-        if len(_FREQ_AXIS) >= 64:
-            _FREQ_AXIS.clear()
-        arr = _FREQ_AXIS[key, n_axes] = (ctypes.c_uint8 * len(key)).from_buffer_copy(key)
-    return arr
-
-
 def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None, inv_freq=None, freq_axis=None,
                           q_weight=None, k_weight=None, weight_offset: float = 0.0, eps: float = 1e-6,
                           norm_qk: bool = True, norm_v: bool = False, q_out=None, workspace=None, stream=None):
@@ -544,111 +534,17 @@ def attn_norm_rope_append(q, k_new, v_new, k_cache, v_cache, dst, positions=None
     [256] of one dtype; q_out: contiguous [n, 8, 256] of any dtype (default: new,
     of the cache's), or q itself.
     """
-    import torch
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    shape, q_stride = q.shape, q.stride()
-    n = shape[0]
-    if shape != (n, N_Q_HEADS, HEAD_DIM) or q_stride[2] != 1 or q_stride[1] != HEAD_DIM:
-        raise ValueError("q must be [n, 8, 256] with each token's values contiguous")
-    in_dtype, row, row1 = q.dtype, (n, HEAD_DIM), (n, 1, HEAD_DIM)
-    k_stride, v_stride = k_new.stride(), v_new.stride()
-    k_shape, v_shape = k_new.shape, v_new.shape
-    if ((k_shape != row and k_shape != row1) or (v_shape != row and v_shape != row1) or k_stride[-1] != 1
-            or v_stride[-1] != 1 or k_new.dtype is not in_dtype or v_new.dtype is not in_dtype
-            or k_new.get_device() != dev or v_new.get_device() != dev):
-        raise ValueError(f"k_new and v_new must be [n, 256] of q's dtype on {q.device}, each token's values contiguous")
-    if (k_cache.get_device() != dev or not k_cache.is_contiguous() or v_cache.get_device() != dev
-            or not v_cache.is_contiguous() or (workspace is not None and _off(workspace, dev))):
-        _need(q.device, k_cache=k_cache, v_cache=v_cache, workspace=workspace)
-    shape = k_cache.shape
-    if shape != v_cache.shape or shape[-1] != HEAD_DIM or k_cache.dtype is not v_cache.dtype:
-        raise ValueError("k_cache and v_cache must be alike, with a last axis of 256")
-    n_axes, pos_p, inv_p = 1, None, None
-    if positions is not None:
-        if inv_freq is None:
-            raise ValueError("give both positions and inv_freq, or neither")
-        shape = positions.shape
-        if len(shape) == 2:
-            n_axes = shape[0]
-        if (positions.get_device() != dev or not positions.is_contiguous() or inv_freq.get_device() != dev
-                or not inv_freq.is_contiguous()):
-            _need(q.device, positions=positions, inv_freq=inv_freq)
-        if positions.dtype is not torch.int64 or (shape != (n_axes, n) and shape != (n,)):
-            raise ValueError("positions must be int64 [n] or [axes, n]")
-        if inv_freq.dtype is not torch.float32 or inv_freq.numel() != HEAD_DIM // 2:
-            raise ValueError("inv_freq must be float32 [128]")
-        pos_p, inv_p = positions.data_ptr(), inv_freq.data_ptr()
-    elif inv_freq is not None:
-        raise ValueError("give both positions and inv_freq, or neither")
-    wt = k_weight if q_weight is None else q_weight
-    wq_p = wk_p = None
-    if q_weight is not None:
-        if q_weight.numel() != HEAD_DIM or q_weight.get_device() != dev or not q_weight.is_contiguous():
-            _need(q.device, q_weight=q_weight)
-            raise ValueError("q_weight must be [256]")
-        wq_p = q_weight.data_ptr()
-    if k_weight is not None:
-        if (k_weight.numel() != HEAD_DIM or k_weight.dtype is not wt.dtype or k_weight.get_device() != dev
-                or not k_weight.is_contiguous()):
-            _need(q.device, k_weight=k_weight)
-            raise ValueError("q_weight and k_weight must be [256] of one dtype")
-        wk_p = k_weight.data_ptr()
     if q_out is None:
-        q_out = torch.empty((n, N_Q_HEADS, HEAD_DIM), dtype=k_cache.dtype, device=q.device)
-    elif (q_out.numel() != n * N_Q_HEADS * HEAD_DIM or q_out.get_device() != dev or not q_out.is_contiguous()):
-        _need(q.device, q_out=q_out)
-        raise ValueError("q_out must be [n, 8, 256]")
-    if isinstance(dst, int):
-        dst_p, dst0 = None, dst
-    else:
-        if (dst.dtype is not torch.int64 or dst.numel() != n or dst.get_device() != dev or not dst.is_contiguous()):
-            raise ValueError("dst must be an int or a contiguous int64 CUDA tensor [n]")
-        dst_p, dst0 = dst.data_ptr(), 0
-    _run(dev, "attn_norm_rope_append", (
-        q.data_ptr(), q_stride[0], k_new.data_ptr(), k_stride[0], v_new.data_ptr(), v_stride[0], dtype_code(q), n,
-        (NORM_QK if norm_qk else 0) | (NORM_V if norm_v else 0), wq_p, wk_p, F32 if wt is None else dtype_code(wt),
-        weight_offset, eps, pos_p, n_axes, _freq_axis(freq_axis, n_axes), inv_p, q_out.data_ptr(), dtype_code(q_out),
-        k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), k_cache.numel() // HEAD_DIM, dst_p, dst0,
-        _ptr(workspace), _cuda_stream(stream, dev)))
+        q_out = q.new_empty(q.shape, dtype=k_cache.dtype)
+    st = _calls().norm_rope_append(
+        _entry("attn_norm_rope_append"), q, k_new, v_new, k_cache, v_cache, dst, positions, inv_freq, freq_axis, q_weight,
+        k_weight, weight_offset, eps, norm_qk, norm_v, q_out, workspace, None if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise KcaError(st, "attn_norm_rope_append")
     return q_out
 
 
 # ------------------------------------------------------ shared-prefix decode
-
-def _out_dtype(q, out):
-    """`out`, or a new float32 tensor of q's shape, and its dtype code."""
-    import torch
-    if out is None:
-        return torch.empty(q.shape, dtype=torch.float32, device=q.device), F32
-    dt = out.dtype
-    if out.numel() != q.numel() or (dt is not q.dtype and dt is not torch.float32):
-        raise ValueError("out must have q's shape and be float32 or of q's dtype")
-    return out, F32 if dt is torch.float32 else dtype_code(out)
-
-
-def _device_lengths(ctx_len_dev, batch: int):
-    import torch
-    if ctx_len_dev.dtype is not torch.int64 or ctx_len_dev.numel() != batch:
-        raise ValueError("ctx_len_dev must be int64 with one entry per sequence")
-
-
-def _queries(q) -> int:
-    """Batch of decode queries [batch, 8, 256]; q's device is checked elsewhere."""
-    batch = q.shape[0]
-    if q.numel() != batch * N_Q_HEADS * HEAD_DIM:
-        raise ValueError("q must be [batch, 8, 256]")
-    return batch
-
-
-def _cache_shape(k_cache, v_cache, batch: int) -> int:
-    """Capacity of a batched cache [batch, capacity, 256] (or [.., 1, 256])."""
-    shape = k_cache.shape
-    if shape[0] != batch or v_cache.shape != shape or k_cache.numel() != batch * shape[1] * HEAD_DIM:
-        raise ValueError("q, k_cache and v_cache must agree in batch and shape, [batch, capacity, 256]")
-    return shape[1]
-
 
 def attn_decode_prefix_workspace_bytes(q_dtype: int, kv_dtype: int, prefix_len: int, ctx_len, window: int = 0) -> int:
     """Workspace of attn_decode_prefix (with device lengths: ask for
@@ -670,49 +566,22 @@ def attn_decode_prefix(q, prefix_k, prefix_v, prefix_len: int, k_cache, v_cache,
     host ints or as an int64 CUDA tensor with the host bound ctx_bound; out:
     float32 (the default) or of q's dtype.  Returns out [batch, 8, 256].
     """
-    import torch
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    batch = _queries(q)
-    on_device = hasattr(ctx_len, "is_cuda") and ctx_len.is_cuda
-    if (not q.is_contiguous() or _off(prefix_k, dev) or _off(prefix_v, dev) or k_cache.get_device() != dev
-            or not k_cache.is_contiguous() or v_cache.get_device() != dev or not v_cache.is_contiguous()
-            or _off(out, dev) or _off(workspace, dev) or (on_device and _off(ctx_len, dev))):
-        _need(q.device, q=q, prefix_k=prefix_k, prefix_v=prefix_v, k_cache=k_cache, v_cache=v_cache, out=out,
-              workspace=workspace, ctx_len=ctx_len if on_device else None)
-    capacity = _cache_shape(k_cache, v_cache, batch)
-    if prefix_len > 0 and (prefix_k is None or prefix_v is None):
-        raise ValueError("a prefix of more than 0 rows needs prefix_k and prefix_v")
-    kv = k_cache.dtype
-    if v_cache.dtype != kv:
-        raise TypeError("the prefix and the caches must share a dtype")
-    for t in (prefix_k, prefix_v):
-        if t is not None:
-            if t.dtype != kv:
-                raise TypeError("the prefix and the caches must share a dtype")
-            if t.numel() < prefix_len * HEAD_DIM:
-                raise ValueError("the prefix has fewer than prefix_len rows")
-    out, od = _out_dtype(q, out)
-    qd, kd = dtype_code(q), dtype_code(k_cache)
-    if on_device:
-        _device_lengths(ctx_len, batch)
-        if ctx_bound is None:
-            ctx_bound = min(prefix_len + capacity, MAX_POSITION)
-        host_p, dev_p = None, ctx_len.data_ptr()
-    else:
-        nctx, host_p = _i64_array(ctx_len)
-        if nctx != batch:
-            raise ValueError("ctx_len must have one entry per sequence")
-        dev_p, ctx_bound = None, 0
+    if out is None:
+        out = _f32_like(q)
     if workspace is None:
-        with torch.cuda.device(dev):
-            workspace = new_workspace(attn_decode_prefix_workspace_bytes(
-                qd, kd, prefix_len, [ctx_bound] * batch if on_device else ctx_len, window), q.device, stream)
-    _run(dev, "attn_decode_prefix", (
-        q.data_ptr(), qd, _ptr(prefix_k), _ptr(prefix_v), prefix_len, k_cache.data_ptr(), v_cache.data_ptr(), kd,
-        N_Q_HEADS, N_KV_HEADS, HEAD_DIM, capacity, batch, host_p, dev_p, ctx_bound, window, scale, out.data_ptr(), od,
-        workspace.data_ptr(), workspace.numel(), _cuda_stream(stream, dev)))
+        import torch
+        batch = q.shape[0]
+        if isinstance(ctx_len, torch.Tensor) and ctx_len.is_cuda:
+            lengths = [min(prefix_len + k_cache.shape[1], MAX_POSITION) if ctx_bound is None else ctx_bound] * batch
+        else:
+            lengths = ctx_len
+        workspace = _workspace_for(q, lambda: attn_decode_prefix_workspace_bytes(
+            dtype_code(q), dtype_code(k_cache), prefix_len, lengths, window), stream)
+    st = _calls().decode_prefix(
+        _entry("attn_decode_prefix"), q, prefix_k, prefix_v, prefix_len, k_cache, v_cache, ctx_len, window, scale, ctx_bound,
+        out, workspace, None if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise KcaError(st, "attn_decode_prefix")
     return out
 
 
@@ -726,30 +595,17 @@ def attn_summarize_blocks(k_cache, ctx_len_dev, n_new: int, codes=None, scales=N
     float32 [batch, ceil(capacity / 64)] (default: new and zero), in which the
     other blocks stay as they are.  Returns codes, scales.
     """
-    import torch
-    dev = k_cache.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    batch, capacity = k_cache.shape[:2]
-    blocks = -(-capacity // BLOCK_KEYS)
-    if codes is None:
-        codes = torch.zeros((batch, blocks, 2, HEAD_DIM), dtype=torch.int8, device=k_cache.device)
-    if scales is None:
-        scales = torch.zeros((batch, blocks), dtype=torch.float32, device=k_cache.device)
-    if (not k_cache.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
-            or codes.get_device() != dev or not codes.is_contiguous() or scales.get_device() != dev
-            or not scales.is_contiguous() or _off(workspace, dev)):
-        _need(k_cache.device, k_cache=k_cache, ctx_len_dev=ctx_len_dev, codes=codes, scales=scales, workspace=workspace)
-    _device_lengths(ctx_len_dev, batch)
-    if k_cache.numel() != batch * capacity * HEAD_DIM:
-        raise ValueError("k_cache must be [batch, capacity, 256]")
-    if codes.dtype is not torch.int8 or codes.numel() != batch * blocks * 2 * HEAD_DIM:
-        raise ValueError("codes must be int8 [batch, ceil(capacity / 64), 2, 256]")
-    if scales.dtype is not torch.float32 or scales.numel() != batch * blocks:
-        raise ValueError("scales must be float32 [batch, ceil(capacity / 64)]")
-    _run(dev, "attn_summarize_blocks", (
-        k_cache.data_ptr(), dtype_code(k_cache), capacity, batch, ctx_len_dev.data_ptr(), n_new, codes.data_ptr(),
-        scales.data_ptr(), _ptr(workspace), _cuda_stream(stream, dev)))
+    if codes is None or scales is None:
+        import torch
+        blocks = (k_cache.shape[0], -(-k_cache.shape[1] // BLOCK_KEYS))
+        if codes is None:
+            codes = k_cache.new_zeros((*blocks, 2, HEAD_DIM), dtype=torch.int8)
+        if scales is None:
+            scales = k_cache.new_zeros(blocks, dtype=torch.float32)
+    st = _calls().summarize_blocks(_entry("attn_summarize_blocks"), k_cache, ctx_len_dev, n_new, codes, scales, workspace,
+                                   None if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise KcaError(st, "attn_summarize_blocks")
     return codes, scales
 
 
@@ -769,31 +625,15 @@ def attn_select_blocks(q, codes, scales, ctx_len_dev, ctx_bound: int, n_select: 
     last n_recent blocks are always taken.  Returns blocks int32
     [batch, n_select], ascending, -1 behind the last.
     """
-    import torch
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    batch = _queries(q)
     if blocks is None:
-        blocks = torch.empty((batch, n_select), dtype=torch.int32, device=q.device)
-    if (not q.is_contiguous() or codes.get_device() != dev or not codes.is_contiguous() or scales.get_device() != dev
-            or not scales.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
-            or blocks.get_device() != dev or not blocks.is_contiguous() or _off(workspace, dev)):
-        _need(q.device, q=q, codes=codes, scales=scales, ctx_len_dev=ctx_len_dev, blocks=blocks, workspace=workspace)
-    _device_lengths(ctx_len_dev, batch)
-    shape = scales.shape
-    if (codes.dtype is not torch.int8 or scales.dtype is not torch.float32 or len(shape) != 2 or shape[0] != batch
-            or codes.numel() != scales.numel() * 2 * HEAD_DIM):
-        raise ValueError("codes must be int8 [batch, blocks, 2, 256] and scales float32 [batch, blocks]")
-    if blocks.dtype is not torch.int32 or blocks.numel() != batch * n_select:
-        raise ValueError("blocks must be int32 [batch, n_select]")
+        import torch
+        blocks = q.new_empty((q.shape[0], n_select), dtype=torch.int32)
     if workspace is None:
-        with torch.cuda.device(dev):
-            workspace = new_workspace(attn_select_blocks_workspace_bytes(batch, ctx_bound), q.device, stream)
-    _run(dev, "attn_select_blocks", (
-        q.data_ptr(), dtype_code(q), codes.data_ptr(), scales.data_ptr(), shape[1], batch, ctx_len_dev.data_ptr(),
-        ctx_bound, n_select, n_sink, n_recent, blocks.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _cuda_stream(stream, dev)))
+        workspace = _workspace_for(q, lambda: attn_select_blocks_workspace_bytes(q.shape[0], ctx_bound), stream)
+    st = _calls().select_blocks(_entry("attn_select_blocks"), q, codes, scales, ctx_len_dev, ctx_bound, n_select, n_sink,
+                                n_recent, blocks, workspace, None if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise KcaError(st, "attn_select_blocks")
     return blocks
 
 
@@ -813,33 +653,14 @@ def attn_decode_blocks(q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound: int,
     [batch], each 0..ctx_bound; out: float32 (the default) or of q's dtype.
     Returns out [batch, 8, 256].
     """
-    import torch
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    batch = _queries(q)
-    if (not q.is_contiguous() or k_cache.get_device() != dev or not k_cache.is_contiguous()
-            or v_cache.get_device() != dev or not v_cache.is_contiguous() or blocks.get_device() != dev
-            or not blocks.is_contiguous() or ctx_len_dev.get_device() != dev or not ctx_len_dev.is_contiguous()
-            or _off(out, dev) or _off(workspace, dev)):
-        _need(q.device, q=q, k_cache=k_cache, v_cache=v_cache, blocks=blocks, ctx_len_dev=ctx_len_dev, out=out,
-              workspace=workspace)
-    _device_lengths(ctx_len_dev, batch)
-    capacity = _cache_shape(k_cache, v_cache, batch)
-    if k_cache.dtype is not v_cache.dtype:
-        raise TypeError("k_cache and v_cache must share a dtype")
-    shape = blocks.shape
-    if blocks.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch:
-        raise ValueError("blocks must be int32 [batch, n_list]")
-    n_list = shape[1]
-    out, od = _out_dtype(q, out)
+    if out is None:
+        out = _f32_like(q)
     if workspace is None:
-        with torch.cuda.device(dev):
-            workspace = new_workspace(attn_decode_blocks_workspace_bytes(batch, n_list), q.device, stream)
-    _run(dev, "attn_decode_blocks", (
-        q.data_ptr(), dtype_code(q), k_cache.data_ptr(), v_cache.data_ptr(), dtype_code(k_cache), N_Q_HEADS,
-        N_KV_HEADS, HEAD_DIM, capacity, batch, blocks.data_ptr(), n_list, ctx_len_dev.data_ptr(), ctx_bound, scale,
-        out.data_ptr(), od, workspace.data_ptr(), workspace.numel(), _cuda_stream(stream, dev)))
+        workspace = _workspace_for(q, lambda: attn_decode_blocks_workspace_bytes(q.shape[0], blocks.shape[1]), stream)
+    st = _calls().decode_blocks(_entry("attn_decode_blocks"), q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound, scale,
+                                out, workspace, None if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise KcaError(st, "attn_decode_blocks")
     return out
 
 

@@ -5,14 +5,18 @@
 --checked builds libkca_checked.so, the bounds-checked variant.
 
 --verbose passes -Xptxas -v (registers, spills, shared memory per kernel).
+Beside it, g++ builds _kca_torch.so, the native part of the Python binding
+(csrc/kca_torch.cpp), against the headers of this interpreter and of torch.
 The CUDA runtime is linked statically so the library does not depend on the
 runtime version of the host process; streams passed in are driver streams.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -23,6 +27,7 @@ LIB = os.path.join(HERE, "libkca.so")
 # status word instead of making the access; tests run it beside LIB.
 OBJ_CHECKED = os.path.join(HERE, "_build_checked")
 LIB_CHECKED = os.path.join(HERE, "libkca_checked.so")
+BINDING = os.path.join(HERE, "_kca_torch.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -59,9 +64,31 @@ def _compile(src: str, verbose: bool, objdir: str = OBJ, extra=()) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """The native part of the Python binding; needs no GPU and no nvcc."""
+    src = os.path.join(CSRC, "kca_torch.cpp")
+    if not force and os.path.exists(BINDING):
+        if all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (src, os.path.join(INCLUDE, "kca.h"))):
+            return BINDING
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]   # its place, without importing it
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    includes = [sysconfig.get_path("include"), os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), cuda]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-isystem{i}" for i in includes), src,
+           "-o", tmp, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     lib, objdir = (LIB_CHECKED, OBJ_CHECKED) if checked else (LIB, OBJ)
     extra = ("-DKCA_BOUNDS_CHECK",) if checked else ()
+    if not checked:
+        build_binding(force)
     if not force and not verbose and not _stale(lib):
         return lib
     os.makedirs(objdir, exist_ok=True)

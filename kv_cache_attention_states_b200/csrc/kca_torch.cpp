@@ -1,0 +1,375 @@
+// kca_torch.cpp -- argument marshalling of the package's shortest calls: torch
+// tensors in, a call of the C ABI out.  A decode step's norm, block choice or
+// bounds take 2 to 7 us on the GPU, and reading a dozen tensors from Python and
+// converting two dozen arguments takes longer than that (norm + rotation +
+// append: 8.5 us of Python and ctypes, 1 us here).  It holds no arithmetic: every
+// function checks its tensors, puts them in the order of include/kca.h and calls
+// the entry point whose address it is given (so the caller decides which build
+// of the library runs).  Compiled by g++ against the headers of the interpreter
+// and of torch; loaded by __init__.py, whose functions document the arguments.
+#include <Python.h>
+
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <limits>
+#include <vector>
+
+#include "../../include/kca.h"
+
+namespace {
+
+using at::Tensor;
+constexpr int64_t kHeads = KCA_N_Q_HEADS, kDim = KCA_HEAD_DIM;
+
+struct Refused {};   // the Python error is set
+
+[[noreturn]] void refuse(PyObject* type, const char* format, const char* what = "", int device = 0) {
+  PyErr_Format(type, format, what, device);
+  throw Refused{};
+}
+void need(bool ok, const char* message) {
+  if (!ok) refuse(PyExc_ValueError, "%s", message);
+}
+
+// --------------------------------------------------------------- Python values
+const Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a tensor", name);
+  return THPVariable_Unpack(o);
+}
+int64_t whole(PyObject* o) {
+  PyObject* i = PyNumber_Index(o);
+  if (i == nullptr) throw Refused{};
+  const int64_t v = PyLong_AsLongLong(i);
+  Py_DECREF(i);
+  if (v == -1 && PyErr_Occurred()) throw Refused{};
+  return v;
+}
+int32_t whole32(PyObject* o, const char* name) {
+  const int64_t v = whole(o);
+  if (v < std::numeric_limits<int32_t>::min() || v > std::numeric_limits<int32_t>::max())
+    refuse(PyExc_ValueError, "%s out of range", name);
+  return static_cast<int32_t>(v);
+}
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{};
+  return static_cast<float>(v);
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{};
+  return v != 0;
+}
+
+// --------------------------------------------------------------------- tensors
+int device_of(const Tensor& t) {
+  if (!t.is_cuda()) refuse(PyExc_ValueError, "tensors must be CUDA tensors");
+  return t.get_device();
+}
+const Tensor& on(const Tensor& t, int device, const char* name) {
+  if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous())
+    refuse(PyExc_ValueError, "%s must be a contiguous tensor on cuda:%d", name, device);
+  return t;
+}
+const Tensor& on(PyObject* o, int device, const char* name) { return on(tensor(o, name), device, name); }
+// Its address, or null for None.
+void* optional(PyObject* o, int device, const char* name) {
+  return o == Py_None ? nullptr : on(o, device, name).data_ptr();
+}
+int32_t code(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return KCA_F32;
+    case at::kHalf: return KCA_F16;
+    case at::kBFloat16: return KCA_BF16;
+    default: refuse(PyExc_TypeError, "unsupported dtype %s", c10::toString(t.scalar_type()));
+  }
+}
+bool is(const Tensor& t, at::ScalarType s) { return t.scalar_type() == s; }
+// Batch of decode queries [batch, 8, 256].
+int64_t queries(const Tensor& q) {
+  const int64_t batch = q.dim() > 0 ? q.size(0) : 0;
+  need(q.dim() > 0 && q.numel() == batch * kHeads * kDim, "q must be [batch, 8, 256]");
+  need(batch <= std::numeric_limits<int32_t>::max(), "q must be [batch, 8, 256]");
+  return batch;
+}
+// Capacity of a batched cache [batch, capacity, 256].
+int64_t capacity_of(const Tensor& k, const Tensor& v, int64_t batch) {
+  need(k.dim() >= 2 && k.size(0) == batch && v.sizes() == k.sizes() && k.numel() == batch * k.size(1) * kDim,
+       "q, k_cache and v_cache must agree in batch and shape, [batch, capacity, 256]");
+  return k.size(1);
+}
+const int64_t* device_lengths(const Tensor& t, int64_t batch) {
+  need(is(t, at::kLong) && t.numel() == batch, "ctx_len_dev must be int64 with one entry per sequence");
+  return t.data_ptr<int64_t>();
+}
+int32_t out_code(const Tensor& q, const Tensor& out) {
+  need(out.numel() == q.numel() && (is(out, at::kFloat) || out.scalar_type() == q.scalar_type()),
+       "out must have q's shape and be float32 or of q's dtype");
+  return code(out);
+}
+
+// ----------------------------------------------------------------------- calls
+// f(stream) on `device` and the given stream (None: torch's current one there),
+// the interpreter released meanwhile; the entry point's status.
+template <class F>
+PyObject* launch(int device, PyObject* stream, F f) {
+  void* s = stream == Py_None ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream())
+                              : reinterpret_cast<void*>(whole(stream));
+  int status = KCA_OK;
+  PyThreadState* const state = PyEval_SaveThread();
+  try {
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    status = f(s);
+  } catch (...) {
+    PyEval_RestoreThread(state);
+    throw;
+  }
+  PyEval_RestoreThread(state);
+  return PyLong_FromLong(status);
+}
+template <class F>
+F* entry(PyObject* address, F*) {
+  return reinterpret_cast<F*>(whole(address));
+}
+
+// (entry, q, k_new, v_new, k_cache, v_cache, dst, positions, inv_freq, freq_axis,
+//  q_weight, k_weight, weight_offset, eps, norm_qk, norm_v, q_out, workspace, stream)
+PyObject* norm_rope_append(PyObject* const* a) {
+  const Tensor& q = tensor(a[1], "q");
+  const int dev = device_of(q);
+  need(q.dim() == 3 && q.size(1) == kHeads && q.size(2) == kDim && q.stride(2) == 1 && q.stride(1) == kDim &&
+           q.size(0) <= std::numeric_limits<int32_t>::max(),
+       "q must be [n, 8, 256] with each token's values contiguous");
+  const int64_t n = q.size(0);
+  auto row = [&](PyObject* o, const char* name) -> const Tensor& {
+    const Tensor& t = tensor(o, name);
+    const int64_t d = t.dim();
+    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != q.scalar_type() || (d != 2 && d != 3) ||
+        t.size(0) != n || t.size(d - 1) != kDim || (d == 3 && t.size(1) != 1) || t.stride(d - 1) != 1)
+      refuse(PyExc_ValueError, "%s must be [n, 256] of q's dtype on cuda:%d, each token's values contiguous", name, dev);
+    return t;
+  };
+  const Tensor &k = row(a[2], "k_new"), &v = row(a[3], "v_new");
+  const Tensor &kc = on(a[4], dev, "k_cache"), &vc = on(a[5], dev, "v_cache");
+  need(kc.dim() > 0 && kc.sizes() == vc.sizes() && kc.size(kc.dim() - 1) == kDim && kc.scalar_type() == vc.scalar_type(),
+       "k_cache and v_cache must be alike, with a last axis of 256");
+  need((a[7] == Py_None) == (a[8] == Py_None), "give both positions and inv_freq, or neither");
+  int64_t n_axes = 1;
+  const int64_t* pos = nullptr;
+  const float* inv = nullptr;
+  if (a[7] != Py_None) {
+    const Tensor &p = on(a[7], dev, "positions"), &f = on(a[8], dev, "inv_freq");
+    if (p.dim() == 2) n_axes = p.size(0);
+    need(is(p, at::kLong) && (p.dim() == 1 || p.dim() == 2) && p.size(p.dim() - 1) == n && n_axes <= KCA_MAX_ROPE_AXES,
+         "positions must be int64 [n] or [axes, n], with at most 4 axes");
+    need(is(f, at::kFloat) && f.numel() == kDim / 2, "inv_freq must be float32 [128]");
+    pos = p.data_ptr<int64_t>();
+    inv = f.data_ptr<float>();
+  }
+  uint8_t axis[kDim / 2];
+  const bool axes = a[9] != Py_None;
+  if (axes) {
+    PyObject* s = PySequence_Fast(a[9], "freq_axis must be a sequence of axis numbers");
+    if (s == nullptr) throw Refused{};
+    bool ok = PySequence_Fast_GET_SIZE(s) == kDim / 2;
+    for (int i = 0; ok && i < kDim / 2; ++i) {
+      const long x = PyLong_AsLong(PySequence_Fast_GET_ITEM(s, i));
+      ok = x >= 0 && x < n_axes;
+      axis[i] = static_cast<uint8_t>(x);
+    }
+    Py_DECREF(s);
+    if (PyErr_Occurred()) throw Refused{};
+    need(ok, "freq_axis must give one of the axes of positions for each of 128 frequencies");
+  }
+  const void* weight[2] = {nullptr, nullptr};
+  int32_t w_dtype = KCA_F32;
+  for (int i = 0; i < 2; ++i) {
+    if (a[10 + i] == Py_None) continue;
+    const Tensor& w = on(a[10 + i], dev, i == 0 ? "q_weight" : "k_weight");
+    need(w.numel() == kDim && (i == 0 || weight[0] == nullptr || code(w) == w_dtype),
+         "q_weight and k_weight must be [256] of one dtype");
+    w_dtype = code(w);
+    weight[i] = w.data_ptr();
+  }
+  const float w0 = real(a[12]), eps = real(a[13]);
+  const int32_t flags = (truth(a[14]) ? KCA_NORM_QK : 0) | (truth(a[15]) ? KCA_NORM_V : 0);
+  const Tensor& out = on(a[16], dev, "q_out");
+  need(out.numel() == n * kHeads * kDim, "q_out must be [n, 8, 256]");
+  const int64_t* dst = nullptr;
+  int64_t dst0 = 0;
+  if (THPVariable_Check(a[6])) {
+    const Tensor& d = on(a[6], dev, "dst");
+    need(is(d, at::kLong) && d.numel() == n, "dst must be an int or a contiguous int64 CUDA tensor [n]");
+    dst = d.data_ptr<int64_t>();
+  } else {
+    dst0 = whole(a[6]);
+  }
+  void* ws = optional(a[17], dev, "workspace");
+  const int32_t in = code(q), od = code(out), kd = code(kc);
+  auto* f = entry(a[0], &attn_norm_rope_append);
+  return launch(dev, a[18], [&](void* s) {
+    return f(q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), in, (int32_t)n, flags,
+             weight[0], weight[1], w_dtype, w0, eps, pos, (int32_t)n_axes, axes ? axis : nullptr, inv, out.data_ptr(), od,
+             kc.data_ptr(), vc.data_ptr(), kd, kc.numel() / kDim, dst, dst0, ws, s);
+  });
+}
+
+// (entry, q, prefix_k, prefix_v, prefix_len, k_cache, v_cache, ctx_len, window,
+//  scale, ctx_bound, out, workspace, stream)
+PyObject* decode_prefix(PyObject* const* a) {
+  const Tensor& q = tensor(a[1], "q");
+  const int dev = device_of(q);
+  on(q, dev, "q");
+  const int64_t batch = queries(q), prefix = whole(a[4]);
+  const Tensor &k = on(a[5], dev, "k_cache"), &v = on(a[6], dev, "v_cache");
+  const int64_t capacity = capacity_of(k, v, batch);
+  need(prefix <= 0 || (a[2] != Py_None && a[3] != Py_None), "a prefix of more than 0 rows needs prefix_k and prefix_v");
+  const void* rows[2] = {nullptr, nullptr};
+  if (v.scalar_type() != k.scalar_type()) refuse(PyExc_TypeError, "the prefix and the caches must share a dtype");
+  for (int i = 0; i < 2; ++i) {
+    if (a[2 + i] == Py_None) continue;
+    const Tensor& t = on(a[2 + i], dev, i == 0 ? "prefix_k" : "prefix_v");
+    if (t.scalar_type() != k.scalar_type()) refuse(PyExc_TypeError, "the prefix and the caches must share a dtype");
+    need(prefix <= t.numel() / kDim, "the prefix has fewer than prefix_len rows");
+    rows[i] = t.data_ptr();
+  }
+  const Tensor& out = on(a[11], dev, "out");
+  const int32_t qd = code(q), kd = code(k), od = out_code(q, out), window = whole32(a[8], "window");
+  const float scale = real(a[9]);
+  const int64_t* on_device = nullptr;
+  int64_t bound = 0;
+  std::vector<int64_t> host;
+  if (THPVariable_Check(a[7]) && THPVariable_Unpack(a[7]).is_cuda()) {
+    on_device = device_lengths(on(a[7], dev, "ctx_len"), batch);
+    bound = a[10] != Py_None                     ? whole(a[10])
+            : prefix < KCA_MAX_POSITION - capacity ? prefix + capacity
+                                                   : KCA_MAX_POSITION;
+  } else {
+    PyObject* s = PySequence_Fast(a[7], "ctx_len must be host integers or an int64 CUDA tensor");
+    if (s == nullptr) throw Refused{};
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(s);
+    host.reserve(static_cast<size_t>(n));
+    try {
+      for (Py_ssize_t i = 0; i < n; ++i) host.push_back(whole(PySequence_Fast_GET_ITEM(s, i)));
+    } catch (...) {
+      Py_DECREF(s);
+      throw;
+    }
+    Py_DECREF(s);
+    need(n == batch, "ctx_len must have one entry per sequence");
+  }
+  const Tensor& ws = on(a[12], dev, "workspace");
+  auto* f = entry(a[0], &attn_decode_prefix);
+  return launch(dev, a[13], [&](void* s) {
+    return f(q.data_ptr(), qd, rows[0], rows[1], prefix, k.data_ptr(), v.data_ptr(), kd, KCA_N_Q_HEADS, KCA_N_KV_HEADS,
+             KCA_HEAD_DIM, capacity, (int32_t)batch, on_device != nullptr ? nullptr : host.data(), on_device, bound, window,
+             scale, out.data_ptr(), od, ws.data_ptr(), (size_t)ws.nbytes(), s);
+  });
+}
+
+// (entry, k_cache, ctx_len_dev, n_new, codes, scales, workspace, stream)
+PyObject* summarize_blocks(PyObject* const* a) {
+  const Tensor& k = tensor(a[1], "k_cache");
+  const int dev = device_of(k);
+  on(k, dev, "k_cache");
+  need(k.dim() >= 2 && k.numel() == k.size(0) * k.size(1) * kDim, "k_cache must be [batch, capacity, 256]");
+  const int64_t batch = k.size(0), capacity = k.size(1), blocks = (capacity + KCA_BLOCK_KEYS - 1) / KCA_BLOCK_KEYS;
+  need(batch <= std::numeric_limits<int32_t>::max(), "k_cache must be [batch, capacity, 256]");
+  const int64_t* ctx = device_lengths(on(a[2], dev, "ctx_len_dev"), batch);
+  const int64_t n_new = whole(a[3]);
+  const Tensor &codes = on(a[4], dev, "codes"), &scales = on(a[5], dev, "scales");
+  need(is(codes, at::kChar) && codes.numel() == batch * blocks * 2 * kDim,
+       "codes must be int8 [batch, ceil(capacity / 64), 2, 256]");
+  need(is(scales, at::kFloat) && scales.numel() == batch * blocks, "scales must be float32 [batch, ceil(capacity / 64)]");
+  void* ws = optional(a[6], dev, "workspace");
+  const int32_t kd = code(k);
+  auto* f = entry(a[0], &attn_summarize_blocks);
+  return launch(dev, a[7], [&](void* s) {
+    return f(k.data_ptr(), kd, capacity, (int32_t)batch, ctx, n_new, codes.data_ptr<int8_t>(), scales.data_ptr<float>(), ws,
+             s);
+  });
+}
+
+// (entry, q, codes, scales, ctx_len_dev, ctx_bound, n_select, n_sink, n_recent,
+//  blocks, workspace, stream)
+PyObject* select_blocks(PyObject* const* a) {
+  const Tensor& q = tensor(a[1], "q");
+  const int dev = device_of(q);
+  on(q, dev, "q");
+  const int64_t batch = queries(q);
+  const Tensor &codes = on(a[2], dev, "codes"), &scales = on(a[3], dev, "scales");
+  need(is(codes, at::kChar) && is(scales, at::kFloat) && scales.dim() == 2 && scales.size(0) == batch &&
+           codes.numel() == scales.numel() * 2 * kDim,
+       "codes must be int8 [batch, blocks, 2, 256] and scales float32 [batch, blocks]");
+  const int64_t* ctx = device_lengths(on(a[4], dev, "ctx_len_dev"), batch);
+  const int64_t bound = whole(a[5]);
+  const int32_t n = whole32(a[6], "n_select"), sink = whole32(a[7], "n_sink"), recent = whole32(a[8], "n_recent");
+  const Tensor& blocks = on(a[9], dev, "blocks");
+  need(is(blocks, at::kInt) && blocks.numel() == batch * n, "blocks must be int32 [batch, n_select]");
+  const Tensor& ws = on(a[10], dev, "workspace");
+  const int32_t qd = code(q);
+  auto* f = entry(a[0], &attn_select_blocks);
+  return launch(dev, a[11], [&](void* s) {
+    return f(q.data_ptr(), qd, codes.data_ptr<int8_t>(), scales.data_ptr<float>(), scales.size(1), (int32_t)batch, ctx, bound,
+             n, sink, recent, blocks.data_ptr<int32_t>(), ws.data_ptr(), (size_t)ws.nbytes(), s);
+  });
+}
+
+// (entry, q, k_cache, v_cache, blocks, ctx_len_dev, ctx_bound, scale, out,
+//  workspace, stream)
+PyObject* decode_blocks(PyObject* const* a) {
+  const Tensor& q = tensor(a[1], "q");
+  const int dev = device_of(q);
+  on(q, dev, "q");
+  const int64_t batch = queries(q);
+  const Tensor &k = on(a[2], dev, "k_cache"), &v = on(a[3], dev, "v_cache");
+  const int64_t capacity = capacity_of(k, v, batch);
+  if (v.scalar_type() != k.scalar_type()) refuse(PyExc_TypeError, "k_cache and v_cache must share a dtype");
+  const Tensor& blocks = on(a[4], dev, "blocks");
+  need(is(blocks, at::kInt) && blocks.dim() == 2 && blocks.size(0) == batch &&
+           blocks.size(1) <= std::numeric_limits<int32_t>::max(),
+       "blocks must be int32 [batch, n_list]");
+  const int64_t* ctx = device_lengths(on(a[5], dev, "ctx_len_dev"), batch);
+  const int64_t bound = whole(a[6]);
+  const float scale = real(a[7]);
+  const Tensor &out = on(a[8], dev, "out"), &ws = on(a[9], dev, "workspace");
+  const int32_t qd = code(q), kd = code(k), od = out_code(q, out);
+  auto* f = entry(a[0], &attn_decode_blocks);
+  return launch(dev, a[10], [&](void* s) {
+    return f(q.data_ptr(), qd, k.data_ptr(), v.data_ptr(), kd, KCA_N_Q_HEADS, KCA_N_KV_HEADS, KCA_HEAD_DIM, capacity,
+             (int32_t)batch, blocks.data_ptr<int32_t>(), (int32_t)blocks.size(1), ctx, bound, scale, out.data_ptr(), od,
+             ws.data_ptr(), (size_t)ws.nbytes(), s);
+  });
+}
+
+// No C++ exception leaves a Python entry.
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", N, n);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Refused&) {
+    return nullptr;
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<F, N>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {method<norm_rope_append, 19>("norm_rope_append"), method<decode_prefix, 14>("decode_prefix"),
+                         method<summarize_blocks, 8>("summarize_blocks"), method<select_blocks, 12>("select_blocks"),
+                         method<decode_blocks, 11>("decode_blocks"), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kca_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__kca_torch() { return PyModule_Create(&module); }

@@ -1,0 +1,114 @@
+"""What the binding of the norm + rotation, shared-prefix and block calls refuses
+before the library sees it: tensors of another type, shape, layout or device,
+and values that are not what they should be.  Nothing is launched."""
+import pytest
+import torch
+
+import kv_cache_attention_states_b200 as kca
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup(cuda_ok):
+    kca.lib()
+
+
+def _t(*shape, dtype=torch.float16):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def _norm(**kw):
+    a = dict(q=_t(4, 8, 256), k_new=_t(4, 256), v_new=_t(4, 256), k_cache=_t(9, 256), v_cache=_t(9, 256), dst=0,
+             positions=_t(3, 4, dtype=torch.int64), inv_freq=_t(128, dtype=torch.float32), freq_axis=[i % 3 for i in range(128)],
+             q_weight=_t(256), k_weight=_t(256), q_out=_t(4, 8, 256))
+    a.update(kw)
+    return kca.attn_norm_rope_append(**a)
+
+
+@pytest.mark.parametrize("kw,error", [
+    ({"q": lambda: _t(4, 8, 256).cpu()}, ValueError), ({"q": lambda: _t(4, 2048)}, ValueError),
+    ({"q": lambda: _t(4, 8, 512)[..., ::2]}, ValueError), ({"q": lambda: _t(8, 4, 256).transpose(0, 1)}, ValueError),
+    ({"q": lambda: 3}, TypeError), ({"q": lambda: _t(4, 8, 256, dtype=torch.float64), }, ValueError),
+    ({"k_new": lambda: _t(5, 256)}, ValueError), ({"v_new": lambda: _t(4, 256, dtype=torch.float32)}, ValueError),
+    ({"k_new": lambda: _t(4, 2, 256)}, ValueError), ({"v_new": lambda: _t(256, 4).T}, ValueError),
+    ({"k_cache": lambda: _t(8, 256)}, ValueError), ({"v_cache": lambda: _t(9, 256, dtype=torch.float32)}, ValueError),
+    ({"v_cache": lambda: _t(18, 256)[::2]}, ValueError), ({"k_cache": lambda: _t(9, 256).cpu()}, ValueError),
+    ({"dst": lambda: _t(4, dtype=torch.int32)}, ValueError), ({"dst": lambda: _t(5, dtype=torch.int64)}, ValueError),
+    ({"dst": lambda: 1.5}, TypeError), ({"dst": lambda: 2 ** 70}, OverflowError),
+    ({"positions": lambda: None}, ValueError), ({"inv_freq": lambda: None}, ValueError),
+    ({"positions": lambda: _t(3, 4, dtype=torch.int32)}, ValueError), ({"positions": lambda: _t(3, 5, dtype=torch.int64)}, ValueError),
+    ({"positions": lambda: _t(5, 4, dtype=torch.int64)}, ValueError), ({"inv_freq": lambda: _t(128)}, ValueError),
+    ({"inv_freq": lambda: _t(64, dtype=torch.float32)}, ValueError),
+    ({"freq_axis": lambda: [0] * 127}, ValueError), ({"freq_axis": lambda: [0] * 127 + [3]}, ValueError),
+    ({"freq_axis": lambda: [0] * 127 + [-1]}, ValueError), ({"freq_axis": lambda: [0] * 127 + ["x"]}, TypeError),
+    ({"freq_axis": lambda: 7}, TypeError), ({"q_weight": lambda: _t(255)}, ValueError),
+    ({"k_weight": lambda: _t(256, dtype=torch.float32)}, ValueError), ({"q_weight": lambda: _t(512)[::2]}, ValueError),
+    ({"q_out": lambda: _t(3, 8, 256)}, ValueError), ({"q_out": lambda: _t(4, 8, 256, dtype=torch.int16)}, TypeError),
+    ({"workspace": lambda: torch.zeros(300000, dtype=torch.uint8)}, ValueError), ({"eps": lambda: "x"}, TypeError),
+    ({"eps": lambda: -1.0}, kca.KcaError), ({"dst": lambda: 6}, kca.KcaError)])
+def test_norm_rope_append(kw, error):
+    _norm()
+    with pytest.raises(error):
+        _norm(**{k: f() for k, f in kw.items()})
+
+
+def _prefix(**kw):
+    a = dict(q=_t(2, 8, 256), prefix_k=_t(10, 256), prefix_v=_t(10, 256), prefix_len=10, k_cache=_t(2, 20, 256),
+             v_cache=_t(2, 20, 256), ctx_len=[10, 30])
+    a.update(kw)
+    return kca.attn_decode_prefix(**a)
+
+
+@pytest.mark.parametrize("kw,error", [
+    ({"q": lambda: _t(3, 8, 256)}, ValueError), ({"q": lambda: _t(2, 8, 512)[..., ::2]}, ValueError),
+    ({"prefix_k": lambda: _t(9, 256)}, ValueError), ({"prefix_v": lambda: None}, ValueError),
+    ({"prefix_k": lambda: _t(10, 256, dtype=torch.bfloat16)}, TypeError), ({"v_cache": lambda: _t(2, 21, 256)}, ValueError),
+    ({"v_cache": lambda: _t(2, 20, 256, dtype=torch.float32)}, TypeError), ({"ctx_len": lambda: [10]}, (ValueError, kca.KcaError)),
+    ({"ctx_len": lambda: [10, 31]}, kca.KcaError), ({"ctx_len": lambda: [9, 30]}, kca.KcaError),
+    ({"ctx_len": lambda: torch.tensor([10, 30], dtype=torch.int32, device="cuda")}, ValueError),
+    ({"ctx_len": lambda: torch.tensor([10, 30], device="cuda"), "ctx_bound": lambda: 31}, kca.KcaError),
+    ({"out": lambda: _t(2, 8, 256, dtype=torch.bfloat16)}, ValueError), ({"out": lambda: _t(1, 8, 256)}, ValueError),
+    ({"workspace": lambda: torch.zeros(100, dtype=torch.uint8, device="cuda")}, kca.KcaError),
+    ({"window": lambda: 2 ** 40}, (ValueError, OverflowError, kca.KcaError)), ({"scale": lambda: 0.0}, kca.KcaError)])
+def test_decode_prefix(kw, error):
+    _prefix()
+    with pytest.raises(error):
+        _prefix(**{k: f() for k, f in kw.items()})
+
+
+def test_decode_prefix_takes_lengths_of_any_kind():
+    import numpy as np
+    outs = [_prefix(ctx_len=c) for c in ([10, 30], (10, 30), np.array([10, 30]), torch.tensor([10, 30]),
+                                         torch.tensor([10, 30], device="cuda"))]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def _blocks(name, **kw):
+    i64 = lambda *s: torch.full(s, 100, dtype=torch.int64, device="cuda")   # noqa: E731
+    a = {"summarize": dict(k_cache=_t(2, 200, 256), ctx_len_dev=i64(2), n_new=1, codes=_t(2, 4, 2, 256, dtype=torch.int8),
+                           scales=_t(2, 4, dtype=torch.float32)),
+         "select": dict(q=_t(2, 8, 256), codes=_t(2, 4, 2, 256, dtype=torch.int8), scales=_t(2, 4, dtype=torch.float32),
+                        ctx_len_dev=i64(2), ctx_bound=200, n_select=3),
+         "decode": dict(q=_t(2, 8, 256), k_cache=_t(2, 200, 256), v_cache=_t(2, 200, 256),
+                        blocks=_t(2, 3, dtype=torch.int32), ctx_len_dev=i64(2), ctx_bound=200)}[name]
+    a.update(kw)
+    return {"summarize": kca.attn_summarize_blocks, "select": kca.attn_select_blocks, "decode": kca.attn_decode_blocks}[name](**a)
+
+
+@pytest.mark.parametrize("name,kw,error", [
+    ("summarize", {"k_cache": lambda: _t(2, 200, 128)}, ValueError), ("summarize", {"codes": lambda: _t(2, 3, 2, 256, dtype=torch.int8)}, ValueError),
+    ("summarize", {"codes": lambda: _t(2, 4, 2, 256, dtype=torch.uint8)}, ValueError), ("summarize", {"scales": lambda: _t(2, 4)}, ValueError),
+    ("summarize", {"ctx_len_dev": lambda: _t(3, dtype=torch.int64)}, ValueError), ("summarize", {"n_new": lambda: 0}, kca.KcaError),
+    ("select", {"q": lambda: _t(2, 8, 128)}, ValueError), ("select", {"codes": lambda: _t(2, 5, 2, 256, dtype=torch.int8)}, ValueError),
+    ("select", {"scales": lambda: _t(8, dtype=torch.float32)}, ValueError), ("select", {"blocks": lambda: _t(2, 4, dtype=torch.int32)}, ValueError),
+    ("select", {"n_select": lambda: 1}, kca.KcaError), ("select", {"ctx_bound": lambda: 400}, kca.KcaError),
+    ("select", {"n_sink": lambda: 2 ** 40}, ValueError),
+    ("decode", {"blocks": lambda: _t(2, 3, dtype=torch.int64)}, ValueError), ("decode", {"blocks": lambda: _t(3, 3, dtype=torch.int32)}, ValueError),
+    ("decode", {"blocks": lambda: _t(2, 6, dtype=torch.int32)[:, ::2]}, ValueError), ("decode", {"v_cache": lambda: _t(2, 200, 256, dtype=torch.bfloat16)}, TypeError),
+    ("decode", {"ctx_bound": lambda: 201}, kca.KcaError), ("decode", {"out": lambda: _t(2, 8, 256, dtype=torch.bfloat16)}, ValueError),
+    ("decode", {"workspace": lambda: torch.zeros(24832, dtype=torch.uint8)}, ValueError)])
+def test_blocks(name, kw, error):
+    _blocks(name)
+    with pytest.raises(error):
+        _blocks(name, **{k: f() for k, f in kw.items()})

@@ -44,15 +44,18 @@ def test_refusals(kw, code):
     assert _call(**kw) == code
 
 
-def test_binding_refuses_cpu_tensors_and_bad_axes():
+def test_binding_refuses_cpu_tensors():
     torch = pytest.importorskip("torch")
     z = torch.zeros((2, 8, 256))
     r = torch.zeros((2, 256))
     with pytest.raises(ValueError):
         kca.attn_norm_rope_append(z, r, r, r, r, 0)
-    for bad in ([0] * 127, [0] * 127 + [2], [0] * 129):
-        with pytest.raises(ValueError):
-            kca._freq_axis(bad, 2)
+    with pytest.raises(ValueError):
+        kca.attn_decode_prefix(z, None, None, 0, z, z, [1, 2])
+    with pytest.raises(ValueError):
+        kca.attn_summarize_blocks(z, torch.ones(2, dtype=torch.int64), 1)
+    with pytest.raises(TypeError):
+        kca.attn_norm_rope_append(None, r, r, r, r, 0, q_out=z)
 
 
 def test_oracle_norm_is_scale_free_and_has_unit_mean_square():
