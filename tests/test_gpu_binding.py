@@ -112,3 +112,48 @@ def test_blocks(name, kw, error):
     _blocks(name)
     with pytest.raises(error):
         _blocks(name, **{k: f() for k, f in kw.items()})
+
+
+def test_two_host_threads():
+    """Two threads call at once (the binding lets go of the interpreter during a
+    call), each on its own stream and workspaces; the results are those of one."""
+    import threading
+
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        t = lambda *s: torch.randn(s, generator=g, device="cuda").half()   # noqa: E731
+        d = dict(q=t(3, 8, 256), k=t(3, 700, 256), v=t(3, 700, 256), pk=t(900, 256), pv=t(900, 256), nk=t(3, 256), nv=t(3, 256),
+                 ctx=torch.tensor([700, 300, 64], device="cuda"))
+        d["codes"], d["scales"] = kca.attn_summarize_blocks(d["k"], d["ctx"], 700)
+        d["ws"] = kca.new_workspace(max(kca.attn_select_blocks_workspace_bytes(3, 700),
+                                        kca.attn_decode_blocks_workspace_bytes(3, 4),
+                                        kca.attn_decode_prefix_workspace_bytes(kca.F16, kca.F16, 900, [1600] * 3)))
+        return d
+
+    def work(d, stream, outs, n):
+        with torch.cuda.stream(stream):
+            for _ in range(n):
+                kc, vc = torch.zeros((3, 256), dtype=torch.float16, device="cuda"), torch.zeros((3, 256), dtype=torch.float16, device="cuda")
+                q = kca.attn_norm_rope_append(d["q"], d["nk"], d["nv"], kc, vc, 0)
+                bl = kca.attn_select_blocks(q, d["codes"], d["scales"], d["ctx"], 700, 4, workspace=d["ws"])
+                outs.append((q, kc, bl, kca.attn_decode_blocks(q, d["k"], d["v"], bl, d["ctx"], 700, workspace=d["ws"]),
+                             kca.attn_decode_prefix(q, d["pk"], d["pv"], 900, d["k"], d["v"], [1600, 1000, 900],
+                                                    workspace=d["ws"])))
+
+    data = [inputs(i) for i in range(2)]
+    torch.cuda.synchronize()
+    alone, streams = [[], []], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        work(data[i], streams[i], alone[i], 1)
+        torch.cuda.synchronize()
+    both = [[], []]
+    threads = [threading.Thread(target=work, args=(data[i], streams[i], both[i], 40)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(both[i]) == 40
+        assert all(all(torch.equal(x, y) for x, y in zip(o, alone[i][0])) for o in both[i])
+        assert kca.attn_device_status(data[i]["ws"])[0] == 0
