@@ -351,8 +351,25 @@ __device__ __forceinline__ void merge_own(const RowsArgs& a, const DBars* bars, 
   float M = -INFINITY;
   for (int src = 0; src < C; ++src) M = max_nan(M, bars->rm[src * W + hi]);
   const int64_t base = (int64_t)(unit / a.pre_group) * a.pre_group_step + (unit % a.pre_group) * kHeads + h;
-  float Mp = -INFINITY;
-  for (int s = lane; s < a.pre_items; s += 32) Mp = max_nan(Mp, a.pre_ml[(base + s * a.pre_item_step) * 2]);
+  // The first partials' sums are asked for together with their (m, l), and each
+  // batch before the one ahead of it is used: one latency in place of three.
+  constexpr int NB = W == 8 ? 4 : W == 4 ? 8 : 16;
+  const int items = a.pre_items;
+  const int64_t step = a.pre_item_step * kDim;
+  const float* acc = a.pre_acc + base * kDim + W * jd;
+  auto load_ml = [&](int s) {
+    return s < items ? *reinterpret_cast<const float2*>(a.pre_ml + (base + s * a.pre_item_step) * 2)
+                     : make_float2(-INFINITY, 0.f);
+  };
+  auto load_batch = [&](int s, float (&v)[NB][W]) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load_w<W>(acc + (s + j < items ? s + j : items - 1) * step, v[j]);
+  };
+  float v[NB][W];
+  float2 ml = load_ml(lane);
+  load_batch(0, v);
+  float Mp = ml.x;
+  for (int s = 32 + lane; s < items; s += 32) Mp = max_nan(Mp, load_ml(s).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) Mp = max_nan(Mp, __shfl_xor_sync(0xffffffffu, Mp, o));
   M = max_nan(M, Mp * a.pre_mscale);
@@ -366,32 +383,31 @@ __device__ __forceinline__ void merge_own(const RowsArgs& a, const DBars* bars, 
 #pragma unroll
     for (int e = 0; e < W; ++e) x[e] += f * bars->ro[src * W + hi][W * jd + e];
   }
-  const int64_t step = a.pre_item_step * kDim;
-  for (int s0 = 0; s0 < a.pre_items; s0 += 32) {
-    float f = 0.f, fl = 0.f;
-    if (s0 + lane < a.pre_items) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.pre_ml + (base + (s0 + lane) * a.pre_item_step) * 2);
+  float f = 0.f;   // weight of partial s of every 32
+  for (int s = 0; s < items; s += NB) {
+    if (s % 32 == 0) {
+      if (s > 0) ml = load_ml(s + lane);
       f = exp2f((ml.x * a.pre_mscale - mu) * kDLog2e);
-      fl = f * ml.y;
+      float fl = f * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, o);
+      L += fl;
     }
+    float next[NB][W];
+    if (s + NB < items) load_batch(s + NB, next);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, o);
-    L += fl;
-    const int n = a.pre_items - s0 < 32 ? a.pre_items - s0 : 32;
-    const float* p = a.pre_acc + (base + s0 * a.pre_item_step) * kDim + W * jd;
-    constexpr int NB = W == 8 ? 8 : 16;   // loads in flight
-    for (int s = 0; s < n; s += NB) {
-      float v[NB][W];
+    for (int j = 0; j < NB; ++j) {
+      const float w = __shfl_sync(0xffffffffu, f, (s + j) & 31);
+      if (s + j < items) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) load_w<W>(p + (s + j < n ? s + j : s) * step, v[j]);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const float w = __shfl_sync(0xffffffffu, f, (s + j) & 31);
-        if (s + j < n) {
-#pragma unroll
-          for (int e = 0; e < W; ++e) x[e] += w * v[j][e];
-        }
+        for (int e = 0; e < W; ++e) x[e] += w * v[j][e];
       }
+    }
+    if (s + NB < items) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[j][e] = next[j][e];
     }
   }
   if (nclus == 1) {
