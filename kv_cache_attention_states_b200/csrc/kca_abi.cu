@@ -571,20 +571,22 @@ int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t b
     *out = p;
     return KCA_OK;
   }
-  // The routes' times in microseconds, from B200 graph replays: 5 and the keys
-  // at 6.5 TB/s; or 8.5 for the tiles' launch and 1.65 per 128 keys (17 and 1.1
-  // per 64 keys for units), the own keys, and the partials' way through L2.
-  // Measured, joined against tiles or units: 3 x 1,000 bf16 6.4 / 12.8, 8 x
-  // 8,192 of f32 queries 15.7 / 21.9, 32 x 16,384 bf16 66 / 19.3, 256 x 120,000
-  // f16 3,389 / 204.
+  // The routes' times in microseconds, from B200 graph replays.  Joined: 6 and
+  // the keys at 7.4 TB/s (mostly from L2).  Tiles: 8.9 for both launches and 1.65
+  // per 128 keys of an item (units: 12, and 1.1 per 64), then the merge, in which
+  // a CTA takes 8 / c heads' partials, 1 KiB each, at 30 GB/s; so a shorter pass
+  // over the prefix costs a longer merge, and both are searched.  Measured, joined
+  // against tiles or units: 3 x 1,000 bf16 7.4 / 10.7, 8 x 8,192 bf16 15.3 / 12.3,
+  // 8 x 8,192 of f32 queries 15.5 / 17.1, 8 x 32,768 of them 37.0 / 26.0, 32 x
+  // 16,384 bf16 66 / 18.7, 64 x 120,000 bf16 853 / 62.
   int64_t longest = 1, sum_own = 0, sum_joined = 0;
   for (int32_t b = 0; b < batch; ++b) {
     longest = own[b] > longest ? own[b] : longest;
     sum_own += own[b];
     sum_joined += joined[b];
   }
-  const double t_joined = 5. + (double)sum_joined * 1024. / 6.5e6;
-  double t_own = 1.5 + (double)sum_own * 1024. / 6.5e6;
+  const double t_joined = 6. + (double)sum_joined * 1024. / 7.4e6;
+  double t_own = 4.5 + (double)sum_own * 1024. / 6.5e6;   // their CTAs start when the prefix is done
   if (batch > sms / 2) {   // one CTA a sequence, in waves
     const double waves = (double)((batch + sms - 1) / sms) * (double)longest * 1024. / 50e3;
     if (waves > t_own) t_own = waves;
@@ -601,43 +603,55 @@ int plan_prefix(int32_t q_dtype, int32_t kv_dtype, int64_t prefix_len, int32_t b
     for (int c = 0; c <= 8; c = c == 0 ? 1 : 2 * c) {
       const int left = sms - batch * c;
       if (c > 0 && left < sms / 4) break;
-      double t = 0.;
-      size_t bytes = 0;
-      kca::TcPlan tc{};
-      kca::RowsPlan pre{};
-      int32_t ur = 0;
-      if (p.route == PrefixPlan::kTiles) {
-        tc = kca::make_tc_prefix_plan(p.kv_lo, prefix_len, batch, window, left / 2);
-        if (2 * tc.n_items > left) continue;
-        bytes = slots_bytes((size_t)tc.n_slots * 128);
-        t = 8.5 + 1.65 * tc.per_item;
-      } else {
-        ur = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
-        const int32_t units = (batch + ur - 1) / ur;
-        if (units > left) continue;
-        pre = kca::make_equal_rows_plan(units, prefix_len - p.kv_lo, left, kca::kMultiRowMinSplit);
-        bytes = slots_bytes((size_t)batch * pre.max_splits * kHeads);
-        t = 17. + 1.1 * pre.split_len / kRowsStage;
-      }
       kca::RowsPlan o{};
+      double t_beside = 0.;
+      int share = c;   // CTAs that merge a sequence's heads
       if (c == 0) {
-        t += t_own;
+        for (share = 8; share > 1 && batch * share > sms; share /= 2) {}
       } else {
         o.n_units = batch;
         o.split_len = (int32_t)(kca::cdiv(kca::cdiv(longest, c), kRowsStage) * kRowsStage);
         o.max_splits = kca::rows_n_splits(longest, o.split_len);
-        const double t_beside = 2. + (double)o.split_len * 1024. / 50e3;
-        if (t_beside > t) t = t_beside;
+        t_beside = 2. + (double)o.split_len * 1024. / 50e3;
       }
-      t += 2e6 * (double)bytes / 6.5e12;
-      if (parts != 0 && t >= best) continue;
-      best = t;
-      parts = bytes;
-      p.tc = tc;
-      p.pre = pre;
-      p.unit_rows = ur;
-      p.own = o;
-      cluster = c;
+      int32_t least = 0;   // keys of the shortest pass
+      for (int32_t longer = 1; longer <= 4; ++longer) {
+        kca::TcPlan tc{};
+        kca::RowsPlan pre{};
+        int32_t ur = 0, items = 0;
+        double t = 0.;
+        size_t bytes = 0;
+        if (p.route == PrefixPlan::kTiles) {
+          tc = kca::make_tc_prefix_plan(p.kv_lo, prefix_len, batch, window, left / 2,
+                                        longer == 1 ? kca::kTcMinItemTiles : longer * least);
+          if (longer == 1) least = tc.per_item;
+          if (2 * tc.n_items > left) break;
+          items = tc.max_split;
+          bytes = slots_bytes((size_t)tc.n_slots * 128);
+          t = 8.9 + 1.65 * tc.per_item;
+        } else {
+          ur = batch > kca::kMultiRows ? kca::kMultiRowsWide : kca::kMultiRows;
+          const int32_t units = (batch + ur - 1) / ur;
+          if (units > left) break;
+          pre = kca::make_equal_rows_plan(units, prefix_len - p.kv_lo, left,
+                                          longer == 1 ? kca::kMultiRowMinSplit : longer * least);
+          if (longer == 1) least = pre.split_len;
+          items = pre.max_splits;
+          bytes = slots_bytes((size_t)batch * pre.max_splits * kHeads);
+          t = 12. + 1.1 * pre.split_len / kRowsStage;
+        }
+        if (c == 0) t += t_own;
+        else if (t_beside > t) t = t_beside;
+        t += (double)items * (kHeads / share) / 30. + (double)bytes / 6.5e6;
+        if (parts != 0 && t >= best) continue;
+        best = t;
+        parts = bytes;
+        p.tc = tc;
+        p.pre = pre;
+        p.unit_rows = ur;
+        p.own = o;
+        cluster = c;
+      }
     }
   }
   if (parts == 0 || (forced < 0 && t_joined <= best)) {

@@ -265,9 +265,10 @@ KCA_HD TcItem tc_item(const TcPlan& p, int32_t idx) {
 // Plan of the rows of a batch over a prefix that all of them share: every row
 // tile sees the keys [kv_lo, prefix_len) (a row masks what its window cuts
 // off), every pair gets the same number of items, and every item writes a
-// partial.  Slot of (tile t, item k): t * max_split + k.
+// partial.  Slot of (tile t, item k): t * max_split + k.  min_tiles: fewest key
+// tiles of an item.
 inline TcPlan make_tc_prefix_plan(int64_t kv_lo, int64_t prefix_len, int32_t rows, int32_t window,
-                                  int32_t pair_budget) {
+                                  int32_t pair_budget, int32_t min_tiles) {
   TcPlan p{};
   p.rows = rows;
   p.window = window;
@@ -279,7 +280,7 @@ inline TcPlan make_tc_prefix_plan(int64_t kv_lo, int64_t prefix_len, int32_t row
   int32_t s = (pair_budget > 80 ? 80 : pair_budget) / p.n_pairs;   // 80: the launch's item table
   if (s < 1) s = 1;
   p.per_item = (int32_t)cdiv(n, s);
-  if (p.per_item < kTcMinItemTiles) p.per_item = kTcMinItemTiles;
+  if (p.per_item < min_tiles) p.per_item = min_tiles;
   p.max_split = (int32_t)cdiv(n, p.per_item);
   p.n_items = p.n_pairs * p.max_split;
   p.n_slots = p.n_tiles * p.max_split;
